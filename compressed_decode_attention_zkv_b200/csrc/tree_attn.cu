@@ -1,0 +1,893 @@
+// Attention of a tree of drafted tokens over the compressed cache (sm_100a).
+//
+// Passages: VQKV (gist.science summary of arXiv 2603.16435), section 2.3 "Decoding Stage"
+// (on-demand reconstruction inside attention, local sliding window); VeloxQuant-MLX 0.5.1,
+// "VecInfer" (the rotation is absorbed into the query); Differential-KV README, "Decode & Prefill
+// Innovations" (fp32 log-sum-exp combine).  The tree of drafts has no counterpart on the pages.
+//
+// A (sequence, kv head) pair has R = N * G query rows rho = i * G + g, taken in groups ("items")
+// of kTreeRG = 8.  Four kernels per call (programmatic dependent launches):
+//   1. tree_prepare_kernel  the key lookup tables of every row (query_tables.cuh); the dense part,
+//      one block per item (fp16 window and the drafts that the mask names: partial maximum, sum
+//      and output per row); one block computes the partition of the compressed tokens.
+//   2. tree_scan_kernel     per item and range of tokens: base-2 scores from the tables and the
+//      per-codeword weight histograms W_s[c][row] = sum over the tokens with zv_s = c of
+//      2^(score - ref).  Each (range, item) writes one slot.
+//   3. tree_contract_kernel joins the slots of an item and contracts W_s with the value
+//      codebooks: one part per (stage, half of the codewords).
+//   4. tree_finish_kernel   sums the parts, rotates back, joins the dense part by log-sum-exp.
+#include "query_tables.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace zkv {
+
+constexpr int kTreeRG = 8;           // query rows per item
+constexpr int kTreeUnit = 128;       // tokens per unit of the partition
+constexpr int kTreeMinUnits = 2;     // smallest range of a scan block, in units
+constexpr int kTreeHalves = 2;       // codeword chunks per stage in the contraction
+constexpr int kTreeCw = kCodebook / kTreeHalves;
+constexpr int kTreeTK = 16;          // tokens per thread and tile
+constexpr size_t kTreeSmemMax = 227 * 1024;
+
+struct TreeArgs {
+  QueryTables qt;
+  int B, N, G, Hq, Hkv, Sk, Sv, R, RP, NRG, grid;
+  int64_t Tcap, Wcap, max_comp;
+  const int32_t* n_draft;
+  const __half *dk, *dv;
+  int64_t k_sb, k_sn, k_sh, v_sb, v_sn, v_sh;
+  const uint8_t* mask;
+  int64_t m_sb, m_sn;
+  const uint8_t *k_codes, *v_codes;
+  const int32_t* comp_len;
+  const float* Cv;
+  const __half *win_k, *win_v;
+  const int32_t* win_len;
+  float *out, *lse;
+  int32_t* err;
+  const int32_t* table;
+  int64_t max_pages, n_pages;
+  int pshift;
+  // workspace
+  int64_t* pre;            // [B + 1] units of one item of the sequences before b; then the range
+  float *pw, *pm;          // slots: [slot][Sv][256][8] weights, [slot][8] references
+  float *dm, *dl, *dout;   // dense part per row: maximum (log2), sum, output [D]
+  float *parts;            // [Sv * halves][row][D]
+  float *rm, *rl;          // [row] maximum, [halves][row] sums
+};
+
+// compressed tokens of sequence b that the call reads
+__device__ __forceinline__ int64_t comp_tokens(const int32_t* comp_len, int b, int64_t Tcap,
+                                               int64_t max_comp) {
+  int64_t c = comp_len[b];
+  c = c < 0 ? 0 : c > Tcap ? Tcap : c;
+  return c < max_comp ? c : max_comp;
+}
+
+// ---------------------------------------------------------------------------------------------
+// 1. Tables, dense part, partition
+// ---------------------------------------------------------------------------------------------
+
+template <int D>
+struct TreeDenseSmem {
+  static constexpr int LD = D + 8;          // fp16 row stride: conflict-free 16-byte reads
+  float q[kTreeRG][D];
+  __half k[32 * LD];
+  __half v[32 * LD];
+};
+
+// prefix sums of the sequences' units and the range of one scan block (at least kTreeMinUnits)
+__device__ __forceinline__ void tree_partition(const TreeArgs& a) {
+  __shared__ int64_t ws[kQtThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kQtThreads) {
+    const int b = b0 + tid;
+    int64_t u = 0;
+    if (b < a.B) {
+      const int64_t c = a.comp_len[b];
+      if (c < 0 || c > a.Tcap) set_error(a.err, ZKV_DEVERR_COMP_LEN);
+      const int64_t w = a.win_len[b];
+      if (w < 0 || w > a.Wcap) set_error(a.err, ZKV_DEVERR_WIN_LEN);
+      if (a.n_draft && (a.n_draft[b] < 0 || a.n_draft[b] > a.N)) set_error(a.err, ZKV_DEVERR_DRAFT);
+      u = (comp_tokens(a.comp_len, b, a.Tcap, a.max_comp) + kTreeUnit - 1) / kTreeUnit;
+    }
+    int64_t s = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    if (lane == 31) ws[warp] = s;
+    __syncthreads();
+    int64_t before = base, all = 0;
+    for (int w = 0; w < kQtThreads / 32; ++w) {
+      if (w < warp) before += ws[w];
+      all += ws[w];
+    }
+    if (b < a.B) a.pre[b] = before + s - u;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.pre[a.B] = base;
+    const int64_t total = base * a.Hkv * a.NRG;
+    const int64_t per = (total + a.grid - 1) / a.grid;
+    a.pre[a.B + 1] = per < kTreeMinUnits ? kTreeMinUnits : per;
+  }
+}
+
+// Dense attention of one item: warp = row, lane = key in the scores, head dimensions in the output.
+template <int D>
+__device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t item, TreeDenseSmem<D>& sm) {
+  constexpr int E = D / 32, LD = TreeDenseSmem<D>::LD;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rg = (int)(item % a.NRG);
+  const int64_t pair = item / a.NRG;
+  const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv);
+  const int nd = present_queries(a.n_draft, b, a.N);
+  int64_t wl = a.win_len[b];
+  wl = wl < 0 ? 0 : wl > a.Wcap ? a.Wcap : wl;
+  const int rho = rg * kTreeRG + warp;
+  const int i = rho / a.G;
+  const bool live = rho < a.R && i < nd;
+  if ((rg * kTreeRG) / a.G >= nd) return;      // no row of the block is present (block-uniform)
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    sm.q[warp][e * 32 + lane] =
+        live ? __half2float(a.qt.q[b * a.qt.q_sb + i * a.qt.q_sn +
+                                   ((int64_t)kvh * a.G + rho % a.G) * a.qt.q_sh + e * 32 + lane])
+             : 0.f;
+  const int64_t nk = wl + nd;
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  const uint8_t* mrow = a.mask ? a.mask + b * a.m_sb + (int64_t)(live ? i : 0) * a.m_sn : nullptr;
+  for (int64_t k0 = 0; k0 < nk; k0 += 32) {
+    __syncthreads();
+    for (int f = tid; f < 32 * (D / 8); f += kQtThreads) {
+      const int r = f / (D / 8), c = (f % (D / 8)) * 8;
+      const int64_t t = k0 + r;
+      if (t < nk) {
+        const __half *ks, *vs;
+        if (t < wl) {
+          ks = a.win_k + (pair * a.Wcap + t) * D;
+          vs = a.win_v + (pair * a.Wcap + t) * D;
+        } else {
+          ks = a.dk + b * a.k_sb + (t - wl) * a.k_sn + (int64_t)kvh * a.k_sh;
+          vs = a.dv + b * a.v_sb + (t - wl) * a.v_sn + (int64_t)kvh * a.v_sh;
+        }
+        cp_async16(sm.k + r * LD + c, ks + c);
+        cp_async16(sm.v + r * LD + c, vs + c);
+      }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    const int64_t t = k0 + lane;
+    bool see = live && t < nk;
+    if (see && t >= wl) see = mrow ? mrow[t - wl] != 0 : t - wl <= i;
+    float s0 = 0.f, s1 = 0.f;
+    if (see) {
+#pragma unroll 4
+      for (int c = 0; c < D; c += 8) {
+        const uint4 kv = *reinterpret_cast<const uint4*>(sm.k + lane * LD + c);
+        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[warp][c]);
+        const float4 qb = *reinterpret_cast<const float4*>(&sm.q[warp][c + 4]);
+        const float2 k01 = __half22float2(*reinterpret_cast<const __half2*>(&kv.x));
+        const float2 k23 = __half22float2(*reinterpret_cast<const __half2*>(&kv.y));
+        const float2 k45 = __half22float2(*reinterpret_cast<const __half2*>(&kv.z));
+        const float2 k67 = __half22float2(*reinterpret_cast<const __half2*>(&kv.w));
+        s0 = fmaf(qa.x, k01.x, s0); s1 = fmaf(qa.y, k01.y, s1);
+        s0 = fmaf(qa.z, k23.x, s0); s1 = fmaf(qa.w, k23.y, s1);
+        s0 = fmaf(qb.x, k45.x, s0); s1 = fmaf(qb.y, k45.y, s1);
+        s0 = fmaf(qb.z, k67.x, s0); s1 = fmaf(qb.w, k67.y, s1);
+      }
+    }
+    const float x = see ? (s0 + s1) * a.qt.scale_log2 : -INFINITY;
+    unsigned keys = __ballot_sync(0xffffffffu, see);
+    if (!keys) continue;
+    const float mn = fmaxf(m, warp_max_f32(x));
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float corr = ex2_approx(m - ref);
+    const float p = see ? ex2_approx(x - ref) : 0.f;
+    l = l * corr + warp_sum_f32(p);
+    m = mn;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= corr;
+    while (keys) {      // a key that the row does not see is not multiplied: its value may be NaN
+      const int j = __ffs(keys) - 1;
+      keys &= keys - 1u;
+      const float w = __shfl_sync(0xffffffffu, p, j);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        o[e] = fmaf(w, __half2float(sm.v[j * LD + e * 32 + lane]), o[e]);
+    }
+  }
+  if (!live) return;
+  const int64_t row = pair * a.RP + rho;
+  if (lane == 0) {
+    a.dm[row] = m;
+    a.dl[row] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) a.dout[row * D + e * 32 + lane] = o[e];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kQtThreads) tree_prepare_kernel(TreeArgs a) {
+  extern __shared__ __align__(16) unsigned char smraw[];
+  pdl_trigger();
+  int64_t blk = blockIdx.x;
+  const int64_t nt = a.qt.blocks();
+  if (blk < nt) {
+    query_tables_block<D>(a.qt, blk, *reinterpret_cast<QtSmem<D>*>(smraw));
+  } else if (blk == nt) {
+    tree_partition(a);
+  } else {
+    tree_dense<D>(a, blk - nt - 1, *reinterpret_cast<TreeDenseSmem<D>*>(smraw));
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// 2. Scan
+// ---------------------------------------------------------------------------------------------
+// Lane = (token slot h = lane / 8, row r = lane % 8); a thread takes kTreeTK tokens of a tile for
+// one row.  Shared memory holds 256 rows (codewords) of 256 bytes: bytes [0, 128) the key table
+// entries [stage][copy][row] of the codeword, bytes [128, 256) its weight counters, so that the
+// address of either is one byte permutation [column | code] of the packed codes.  With 8 stages
+// on either side each kind has 256-byte rows of its own.  Slot h visits the stages in the order
+// s = i ^ h (fewer than four stages: copies), so the 32 lanes of every gather and every counter
+// addition lie in 32 distinct banks, whatever the codes are.
+//
+// Weights.  p = 2^(score - ref) with ref the row's maximum over the first tile.  The block sums p
+// per row over the tile before it adds any (one barrier), so a row's unit can be chosen: a power
+// of two with the first tile's sum at 2^27 .. 2^28 units.  Counters then take u = p / unit, rounded,
+// as exact integers in any order; when the sum of a row could pass 2^32 the counters are folded
+// into the slot (float32) and the unit chosen anew.  A rounding is half a unit, 2^-28 of a tile's
+// sum, per token.  A score 2^64 above ref (in p) folds and raises ref.
+template <int SKP, int SVP>
+struct TreeScan {
+  static constexpr bool WIDE = SKP == 8 || SVP == 8;
+  static constexpr int NW = WIDE ? 16 : 8;          // warps
+  static constexpr int THREADS = NW * 32;
+  static constexpr int TILE = NW * 4 * kTreeTK;     // tokens
+  static constexpr int VOFF = WIDE ? 65536 : 128;   // weight counters of a codeword
+  static constexpr int KR = SKP >= 4 ? 1 : 4 / SKP; // copies
+  static constexpr int VR = SVP >= 4 ? 1 : 4 / SVP;
+  static constexpr int SMEM = (WIDE ? 131072 : 65536) + 4 * kTreeRG * NW * 4;
+  static constexpr int KW = SKP <= 4 ? 1 : 2, VW = SVP <= 4 ? 1 : 2;   // code words per token
+};
+
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
+  return __byte_perm(a, b, s);
+}
+
+// The codes of four tokens t .. t + 3 (t a multiple of 4; tokens from tend on read as code 0).
+template <int SP, int W>
+__device__ __forceinline__ void load_four(const CodeRows& rows, uint32_t t, uint32_t tend, int S,
+                                          uint32_t (&w)[4][W]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[u][i] = 0u;
+  if (t >= tend) return;
+  if (S == SP || S == 3) {
+    // four rows lie together (capacities and pages are multiples of 16 tokens), 4 S bytes
+    const uint8_t* p = rows.row(t, S);
+    if (!p) return;
+    const unsigned int* p4 = reinterpret_cast<const unsigned int*>(p);
+    if constexpr (SP == 1) {
+      const uint32_t x = __ldg(p4);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u][0] = (x >> (8 * u)) & 255u;
+    } else if constexpr (SP == 2) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0][0] = x.x & 0xffffu; w[1][0] = x.x >> 16;
+      w[2][0] = x.y & 0xffffu; w[3][0] = x.y >> 16;
+    } else if constexpr (SP == 4) {
+      if (S == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+        w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
+      } else {
+        const uint32_t x = __ldg(p4), y = __ldg(p4 + 1), z = __ldg(p4 + 2);
+        w[0][0] = x & 0xffffffu;
+        w[1][0] = __funnelshift_r(x, y, 24) & 0xffffffu;
+        w[2][0] = __funnelshift_r(y, z, 16) & 0xffffffu;
+        w[3][0] = z >> 8;
+      }
+    } else {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+      w[0][0] = x.x; w[0][W - 1] = x.y; w[1][0] = x.z; w[1][W - 1] = x.w;
+      w[2][0] = y.x; w[2][W - 1] = y.y; w[3][0] = y.z; w[3][W - 1] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (t + u < tend) load_codes<SP>(rows, t + u, S, w[u]);
+  }
+}
+
+template <int SKP, int SVP>
+__global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP>::WIDE ? 1 : 3)
+    tree_scan_kernel(TreeArgs a) {
+  using C = TreeScan<SKP, SVP>;
+  extern __shared__ __align__(16) unsigned char sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane & 7, h = lane >> 3;
+  float* sums = reinterpret_cast<float*>(sm + (C::WIDE ? 131072 : 65536));   // [2][8][NW]
+  float* maxs = sums + 2 * kTreeRG * C::NW;                                  // [2][8][NW]
+  pdl_trigger();
+  // the weight counters start at zero and every fold leaves them at zero
+  for (int f = tid; f < kCodebook * 8; f += C::THREADS) {
+    unsigned char* z = sm + C::VOFF + 256 * (f >> 3) + 16 * (f & 7);
+    *reinterpret_cast<uint4*>(z) = make_uint4(0, 0, 0, 0);
+    if (SVP == 8) *reinterpret_cast<uint4*>(z + 128) = make_uint4(0, 0, 0, 0);
+  }
+  // per-lane columns and selectors: step i of the stage loop
+  uint32_t kcol[(SKP + 1) / 2], vcol[(SVP + 1) / 2], ksel[SKP], vsel[SVP];
+#pragma unroll
+  for (int i = 0; i < (SKP + 1) / 2; ++i) kcol[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < (SVP + 1) / 2; ++i) vcol[i] = 0u;
+#pragma unroll
+  for (int i = 0; i < SKP; ++i) {
+    const uint32_t s = (uint32_t)(i ^ h) & (SKP - 1), rep = SKP >= 4 ? 0u : (uint32_t)h / SKP;
+    kcol[i / 2] |= ((s * C::KR + rep) * 32u + r * 4u) << (8 * (i & 1));
+    ksel[i] = (4u + (i & 1)) | ((s & 3u) << 4) | (6u << 8) | (7u << 12);
+  }
+#pragma unroll
+  for (int i = 0; i < SVP; ++i) {
+    const uint32_t s = (uint32_t)(i ^ h) & (SVP - 1), rep = SVP >= 4 ? 0u : (uint32_t)h / SVP;
+    vcol[i / 2] |= ((s * C::VR + rep) * 32u + r * 4u) << (8 * (i & 1));
+    vsel[i] = (4u + (i & 1)) | ((s & 3u) << 4) | (6u << 8) | (7u << 12);
+  }
+  pdl_wait();
+  const int64_t per = a.pre[a.B + 1];
+  const int64_t items_per_b = (int64_t)a.Hkv * a.NRG;
+  const int64_t total = a.pre[a.B] * items_per_b;
+  int64_t lo = blockIdx.x * per;
+  const int64_t hi = lo + per < total ? lo + per : total;
+  if (lo >= hi) return;
+  // the sequence of the first unit: the last b with pre[b] * items_per_b <= lo
+  int b = 0;
+  {
+    int x = 0, y = a.B;
+    while (y - x > 1) {
+      const int m = (x + y) / 2;
+      if (a.pre[m] * items_per_b <= lo) x = m;
+      else y = m;
+    }
+    b = x;
+  }
+  int buf = 0;
+  while (lo < hi) {
+    int64_t base = a.pre[b] * items_per_b, units = a.pre[b + 1] - a.pre[b];
+    while (units == 0 || lo >= base + units * items_per_b) {
+      ++b;
+      base = a.pre[b] * items_per_b;
+      units = a.pre[b + 1] - a.pre[b];
+    }
+    const int64_t in_b = (lo - base) / units;           // item of the sequence
+    const int64_t off = lo - base - in_b * units;       // its first unit here
+    const int64_t cnt = units - off < hi - lo ? units - off : hi - lo;
+    const int64_t item = b * items_per_b + in_b;
+    const int kvh = (int)(in_b / a.NRG);
+    const int64_t ntok = comp_tokens(a.comp_len, b, a.Tcap, a.max_comp);
+    const uint32_t t0 = (uint32_t)(off * kTreeUnit);
+    const uint32_t tend = (uint32_t)(ntok < (off + cnt) * kTreeUnit ? ntok : (off + cnt) * kTreeUnit);
+    const CodeRows kr = code_rows(a.k_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh,
+                                  a.Hkv, a.Tcap, a.Sk, a.err);
+    const CodeRows vr = code_rows(a.v_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh,
+                                  a.Hkv, a.Tcap, a.Sv, a.err);
+    __syncthreads();   // the previous segment's tables are no longer read
+    {
+      const float* t = a.qt.lut + item * (int64_t)(kCodebook * SKP * kTreeRG);
+      constexpr int Q = SKP * C::KR * 2;    // 16-byte pieces per codeword
+      for (int f = tid; f < kCodebook * Q; f += C::THREADS) {
+        const int c = f / Q, q = f % Q, s = (q >> 1) / C::KR;
+        cp_async16(sm + 256 * c + 16 * q, t + (c * SKP + s) * kTreeRG + 4 * (q & 1));
+      }
+      cp_async_wait_all();
+      __syncthreads();
+    }
+
+    float ref = 0.f, scale = 0.f, unit = 0.f, used = 0.f;
+    bool chosen = false, dirty = false, folded = false, poison = false;
+    float* slot = a.pw + (item + blockIdx.x) * (int64_t)(a.Sv * kCodebook * kTreeRG);
+
+    // score of one token for this lane's row
+    auto score = [&](const uint32_t (&w)[C::KW]) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < SKP; ++i)
+        s += *reinterpret_cast<const float*>(sm + byte_perm(w[i >> 2 < C::KW ? i >> 2 : 0], kcol[i / 2], ksel[i]));
+      return s;
+    };
+    // counters -> slot, times f (a reference that was raised); every thread keeps to its own row
+    auto fold = [&](float f) {
+      for (int x = tid; x < a.Sv * kCodebook * kTreeRG; x += C::THREADS) {
+        const int c = (x >> 3) & (kCodebook - 1), s = x >> 11;
+        uint32_t* p = reinterpret_cast<uint32_t*>(sm + C::VOFF + 256 * c + 32 * (s * C::VR)) + r;
+        float v = 0.f;
+        if (dirty) {
+          // the copies are separate counts of the same word
+#pragma unroll
+          for (int k = 0; k < C::VR; ++k) {
+            v += (float)p[8 * k];
+            p[8 * k] = 0u;
+          }
+          v *= unit;
+        }
+        if (folded) v += slot[x];
+        slot[x] = v * f;
+      }
+      folded = true;
+      dirty = false;
+    };
+
+    // the reference: the row's maximum over the first tile
+    auto publish = [&](float sum, float mx) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      if (lane < 8) {
+        sums[(buf * kTreeRG + r) * C::NW + warp] = sum;
+        maxs[(buf * kTreeRG + r) * C::NW + warp] = mx;
+      }
+      __syncthreads();
+    };
+    auto collect = [&](float& sum, float& mx) {
+      sum = 0.f;
+      mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::NW; w += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(sums + (buf * kTreeRG + r) * C::NW + w);
+        const float4 m4 = *reinterpret_cast<const float4*>(maxs + (buf * kTreeRG + r) * C::NW + w);
+        sum += (s4.x + s4.y) + (s4.z + s4.w);
+        mx = fmaxf(mx, fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
+      }
+      buf ^= 1;
+    };
+    {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k) {
+        const uint32_t t = t0 + ((k * C::NW + warp) * 4 + h) * 4;
+        uint32_t w[4][C::KW];
+        load_four<SKP, C::KW>(kr, t, tend, a.Sk, w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (t + u < tend) mx = fmaxf(mx, score(w[u]));
+      }
+      publish(0.f, mx);
+      float sum;
+      collect(sum, mx);
+      ref = fabsf(mx) < 1e30f ? mx : 0.f;
+    }
+
+    for (uint32_t tile = t0; tile < tend;) {
+      float p[kTreeTK];
+      uint32_t wv[kTreeTK][C::VW];
+      float sum = 0.f, mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k) {
+        const uint32_t t = tile + ((k * C::NW + warp) * 4 + h) * 4;
+        uint32_t wk[4][C::KW], w4[4][C::VW];
+        load_four<SKP, C::KW>(kr, t, tend, a.Sk, wk);
+        load_four<SVP, C::VW>(vr, t, tend, a.Sv, w4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+          for (int i = 0; i < C::VW; ++i) wv[4 * k + u][i] = w4[u][i];
+          const float x = t + u < tend ? score(wk[u]) - ref : -INFINITY;
+          p[4 * k + u] = ex2_approx(x);
+          sum += p[4 * k + u];
+          mx = fmaxf(mx, x);
+        }
+      }
+      publish(sum, mx);
+      collect(sum, mx);
+      // every warp holds all eight rows and the same sums: the votes agree in the whole block
+      const bool up = mx > 64.f && mx < 1e30f;
+      if (__any_sync(0xffffffffu, up)) {
+        // (all additions of the previous tile came before the barrier)
+        fold(up ? ex2_approx(-fminf(mx, 126.f)) : 1.f);
+        if (up && mx > 126.f) {   // 2^-mx is below float32: what the slot holds is nothing
+          for (int x = tid; x < a.Sv * kCodebook * kTreeRG; x += C::THREADS) slot[x] = 0.f;
+        }
+        if (up) ref += mx;
+        chosen = false;
+        __syncthreads();          // the counters are zero before anyone adds
+        continue;                 // the same tile against the new reference
+      }
+      const bool bad = !(sum < 3e38f);
+      poison = poison || bad;
+      const float need = sum * scale + (float)(C::TILE / 2);
+      const bool full = !chosen || used + need > 4.0e9f;
+      if (__any_sync(0xffffffffu, full && !bad)) {
+        if (dirty) {
+          fold(1.f);
+          __syncthreads();
+        }
+        // sum = m 2^e, m in [1/2, 1): unit = 2^(e - 28)
+        int e = (int)((__float_as_uint(sum) >> 23) & 255u) - 126;
+        e = e < -90 ? -90 : e;
+        scale = __uint_as_float((uint32_t)(28 - e + 127) << 23);
+        unit = __uint_as_float((uint32_t)(e - 28 + 127) << 23);
+        used = 0.f;
+        chosen = true;
+      }
+      used += sum * scale + (float)(C::TILE / 2);
+      dirty = true;
+#pragma unroll
+      for (int k = 0; k < kTreeTK; ++k) {
+        const uint32_t u = bad ? 0u : __float2uint_rn(p[k] * scale);
+#pragma unroll
+        for (int i = 0; i < SVP; ++i)
+          atomicAdd(reinterpret_cast<uint32_t*>(
+                        sm + C::VOFF + byte_perm(wv[k][i >> 2 < C::VW ? i >> 2 : 0], vcol[i / 2], vsel[i])), u);
+      }
+      tile += C::TILE;
+    }
+    __syncthreads();
+    fold(1.f);
+    if (warp == 0 && lane < 8)
+      a.pm[(item + blockIdx.x) * kTreeRG + r] = poison ? NAN : ref;
+    lo += cnt;
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// 3. Contraction with the value codebooks
+// ---------------------------------------------------------------------------------------------
+// Block = 8 items of one kv head (64 rows) x one chunk of codewords of one stage.  Warp = item in
+// both steps: it joins the item's slots by their references, then multiplies its 8 rows with the
+// block's codewords (lane = D / 32 head dimensions).
+template <int D>
+struct TreeContractSmem {
+  float cv[kTreeCw][D];
+  float w[8][kTreeCw][kTreeRG];
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) tree_contract_kernel(TreeArgs a) {
+  constexpr int E = D / 32;
+  extern __shared__ __align__(16) unsigned char smraw[];
+  TreeContractSmem<D>& sm = *reinterpret_cast<TreeContractSmem<D>*>(smraw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int part = blockIdx.x % (a.Sv * kTreeHalves);
+  const int s = part / kTreeHalves, half = part % kTreeHalves;
+  const int kvh = blockIdx.y;
+  const int64_t j = (int64_t)(blockIdx.x / (a.Sv * kTreeHalves)) * 8 + warp;   // (b, rg) of kvh
+  pdl_trigger();
+  {
+    const float* cv = a.Cv + (((int64_t)kvh * a.Sv + s) * kCodebook + half * kTreeCw) * D;
+    float* dst = &sm.cv[0][0];
+    for (int f = tid; f < kTreeCw * D / 4; f += 256) cp_async16(dst + 4 * f, cv + 4 * f);
+    cp_async_commit();
+  }
+  pdl_wait();
+  const bool live = j < (int64_t)a.B * a.NRG;
+  int64_t n = 0, row = 0;
+  if (live) {
+    const int b = (int)(j / a.NRG), rg = (int)(j % a.NRG);
+    const int64_t items_per_b = (int64_t)a.Hkv * a.NRG, in_b = (int64_t)kvh * a.NRG + rg;
+    const int64_t units = a.pre[b + 1] - a.pre[b], per = a.pre[a.B + 1];
+    const int64_t p0 = a.pre[b] * items_per_b + in_b * units;
+    const int64_t first = p0 / per;
+    n = units ? (p0 + units - 1) / per - first + 1 : 0;
+    const int64_t slot0 = b * items_per_b + in_b + first;
+    row = ((int64_t)b * a.Hkv + kvh) * a.RP + rg * kTreeRG;
+    // lane holds rows r4 .. r4 + 3 of codewords lane / 2 + 16 k
+    const int r4 = 4 * (lane & 1);
+    float m[4];
+    bool nan[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = -INFINITY, nan[q] = false;
+    for (int64_t k = 0; k < n; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(a.pm + (slot0 + k) * kTreeRG + r4);
+      m[0] = fmaxf(m[0], x.x); m[1] = fmaxf(m[1], x.y);
+      m[2] = fmaxf(m[2], x.z); m[3] = fmaxf(m[3], x.w);
+      nan[0] |= x.x != x.x; nan[1] |= x.y != x.y; nan[2] |= x.z != x.z; nan[3] |= x.w != x.w;
+    }
+    float4 acc[kTreeCw / 16];
+#pragma unroll
+    for (int k = 0; k < kTreeCw / 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t k = 0; k < n; ++k) {
+      const float4 x = *reinterpret_cast<const float4*>(a.pm + (slot0 + k) * kTreeRG + r4);
+      const float4 f = make_float4(ex2_approx(x.x - m[0]), ex2_approx(x.y - m[1]),
+                                   ex2_approx(x.z - m[2]), ex2_approx(x.w - m[3]));
+      const float4* src = reinterpret_cast<const float4*>(
+                              a.pw + (((slot0 + k) * a.Sv + s) * kCodebook + half * kTreeCw) * (int64_t)kTreeRG) + lane;
+#pragma unroll
+      for (int c = 0; c < kTreeCw / 16; ++c) {
+        const float4 v = src[32 * c];
+        acc[c].x = fmaf(f.x, v.x, acc[c].x);
+        acc[c].y = fmaf(f.y, v.y, acc[c].y);
+        acc[c].z = fmaf(f.z, v.z, acc[c].z);
+        acc[c].w = fmaf(f.w, v.w, acc[c].w);
+      }
+    }
+    float l[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < kTreeCw / 16; ++c) {
+      reinterpret_cast<float4*>(&sm.w[warp][0][0])[32 * c + lane] = acc[c];
+      l[0] += acc[c].x; l[1] += acc[c].y; l[2] += acc[c].z; l[3] += acc[c].w;
+    }
+    if (s == 0) {
+      // every token is counted once per stage: the sum of stage 0's weights is the row's sum
+#pragma unroll
+      for (int o = 2; o < 32; o <<= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) l[q] += __shfl_xor_sync(0xffffffffu, l[q], o);
+      if (lane < 2) {
+        const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          a.rl[half * rows + row + r4 + q] = l[q];
+          if (half == 0) a.rm[row + r4 + q] = nan[q] ? NAN : m[q];
+        }
+      }
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  if (!live || n == 0) return;
+  float o[kTreeRG][E];
+#pragma unroll
+  for (int q = 0; q < kTreeRG; ++q)
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[q][e] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < kTreeCw; ++c) {
+    const float4 wa = *reinterpret_cast<const float4*>(&sm.w[warp][c][0]);
+    const float4 wb = *reinterpret_cast<const float4*>(&sm.w[warp][c][4]);
+    const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float v = sm.cv[c][e * 32 + lane];
+#pragma unroll
+      for (int q = 0; q < kTreeRG; ++q) o[q][e] = fmaf(w[q], v, o[q][e]);
+    }
+  }
+  const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
+#pragma unroll
+  for (int q = 0; q < kTreeRG; ++q)
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.parts[(part * rows + row + q) * D + e * 32 + lane] = o[q][e];
+}
+
+// ---------------------------------------------------------------------------------------------
+// 4. Sum of the parts, rotation back, join with the dense part: one warp per row
+// ---------------------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) tree_finish_kernel(TreeArgs a) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  const int64_t x = (int64_t)blockIdx.x * 8 + warp;      // (pair, rho)
+  const int64_t pair = x / a.R;
+  const int rho = (int)(x % a.R);
+  if (pair >= (int64_t)a.B * a.Hkv) return;
+  const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv), i = rho / a.G;
+  if (i >= present_queries(a.n_draft, b, a.N)) return;   // rows behind the drafts stay as they are
+  const int64_t rows = (int64_t)a.B * a.Hkv * a.RP, row = pair * a.RP + rho;
+  const float m = a.rm[row], dm = a.dm[row];
+  float l = a.rl[row];
+#pragma unroll
+  for (int k = 1; k < kTreeHalves; ++k) l += a.rl[k * rows + row];
+  float o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (m != -INFINITY) {
+    for (int p = 0; p < a.Sv * kTreeHalves; ++p)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += a.parts[(p * rows + row) * D + e * 32 + lane];
+    fwht_warp_f32<D>(o, lane);
+  }
+  const float M = fmaxf(m, dm), top = M == -INFINITY ? 0.f : M;
+  const float fc = ex2_approx(m - top), fd = ex2_approx(dm - top);
+  const float total = l * fc + a.dl[row] * fd;
+  const bool none = total == 0.f;
+  const float inv = none ? 0.f : 1.f / total;
+  const float gc = fc * inv * (float)a.qt.rot, gd = fd * inv;
+  const int64_t at = ((int64_t)b * a.N + i) * a.Hq + (int64_t)kvh * a.G + rho % a.G;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    a.out[at * D + e * 32 + lane] =
+        none ? 0.f : fmaf(o[e], gc, a.dout[row * D + e * 32 + lane] * gd);
+  if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------------------------
+
+static int tree_pad_stages(int S) { return S <= 2 ? S : S <= 4 ? 4 : 8; }
+
+struct TreePlan {
+  int R, RP, NRG, SKP, SVP, grid;
+  int64_t items, slots, rows;
+  size_t lut, pre, pw, pm, dm, dl, dout, parts, rm, rl, total;
+};
+
+static TreePlan tree_plan(const zkv_tree_params* p) {
+  TreePlan t{};
+  t.R = p->N * (p->Hq / p->Hkv);
+  t.NRG = (t.R + kTreeRG - 1) / kTreeRG;
+  t.RP = t.NRG * kTreeRG;
+  t.SKP = tree_pad_stages(p->Sk);
+  t.SVP = tree_pad_stages(p->Sv);
+  const int64_t pairs = (int64_t)p->B * p->Hkv;
+  t.items = pairs * t.NRG;
+  t.rows = pairs * t.RP;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 148;
+  const int64_t units = t.items * ((p->max_comp_len + kTreeUnit - 1) / kTreeUnit);
+  const int64_t ctas = (int64_t)sms * (t.SKP == 8 || t.SVP == 8 ? 1 : 3);
+  t.grid = (int)std::max<int64_t>(1, std::min(ctas, (units + kTreeMinUnits - 1) / kTreeMinUnits));
+  t.slots = t.items + t.grid;
+  size_t o = 0;
+  auto take = [&](size_t n) { const size_t at = o; o += align256(n); return at; };
+  t.lut = take(query_tables_bytes(pairs, t.RP, t.SKP));
+  t.pre = take(((size_t)p->B + 2) * 8);
+  t.pw = take((size_t)t.slots * p->Sv * kCodebook * kTreeRG * 4);
+  t.pm = take((size_t)t.slots * kTreeRG * 4);
+  t.dm = take((size_t)t.rows * 4);
+  t.dl = take((size_t)t.rows * 4);
+  t.dout = take((size_t)t.rows * p->d * 4);
+  t.parts = take((size_t)t.rows * p->d * 4 * p->Sv * kTreeHalves);
+  t.rm = take((size_t)t.rows * 4);
+  t.rl = take((size_t)t.rows * 4 * kTreeHalves);
+  t.total = o;
+  return t;
+}
+
+static int validate_tree_shapes(const zkv_tree_params* p) {
+  if (!p) return ZKV_ERR_INVALID_ARG;
+  if (p->B < 1 || p->N < 1 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv) return ZKV_ERR_INVALID_ARG;
+  if (!supported_d(p->d)) return ZKV_ERR_UNSUPPORTED;
+  if (p->Sk < 1 || p->Sk > kMaxStages || p->Sv < 1 || p->Sv > kMaxStages) return ZKV_ERR_UNSUPPORTED;
+  if (p->Hq / p->Hkv > 8 || p->N > 256) return ZKV_ERR_UNSUPPORTED;
+  if (p->B > 65535 || p->Hkv > 65535) return ZKV_ERR_UNSUPPORTED;
+  if ((int64_t)p->B * p->Hkv * p->N > (1 << 24)) return ZKV_ERR_UNSUPPORTED;
+  if (p->Tcap < 0 || p->Wcap < 0 || p->max_comp_len < 0 || p->max_comp_len > p->Tcap)
+    return ZKV_ERR_INVALID_ARG;
+  if (p->Tcap % 16) return ZKV_ERR_INVALID_ARG;
+  if (p->Tcap > (int64_t(1) << 28) || p->Wcap > (int64_t(1) << 28)) return ZKV_ERR_UNSUPPORTED;
+  return validate_paged(p->block_table, p->page_tokens, p->max_pages, p->n_pages, p->Tcap);
+}
+
+static int validate_tree(const zkv_tree_params* p) {
+  const int v = validate_tree_shapes(p);
+  if (v != ZKV_OK) return v;
+  if (!p->q || !p->draft_k || !p->draft_v || !p->comp_len || !p->win_len || !p->out)
+    return ZKV_ERR_INVALID_ARG;
+  if (!p->k_codes || !p->v_codes || !p->k_codebooks || !p->v_codebooks) return ZKV_ERR_INVALID_ARG;
+  if (p->Wcap > 0 && (!p->win_k || !p->win_v)) return ZKV_ERR_INVALID_ARG;
+  const uintptr_t al = (uintptr_t)p->q | (uintptr_t)p->draft_k | (uintptr_t)p->draft_v |
+                       (uintptr_t)p->k_codes | (uintptr_t)p->v_codes | (uintptr_t)p->k_codebooks |
+                       (uintptr_t)p->v_codebooks | (uintptr_t)p->win_k | (uintptr_t)p->win_v;
+  if (al & 15) return ZKV_ERR_INVALID_ARG;
+  const int64_t st[9] = {p->q_sb, p->q_sn, p->q_sh, p->k_sb, p->k_sn, p->k_sh,
+                         p->v_sb, p->v_sn, p->v_sh};
+  for (int64_t s : st)
+    if (s < 0 || s % 8) return ZKV_ERR_INVALID_ARG;
+  if (p->mask && (p->m_sb < 0 || p->m_sn < 0)) return ZKV_ERR_INVALID_ARG;
+  return ZKV_OK;
+}
+
+template <int SKP, int SVP>
+static cudaError_t launch_tree_scan(const TreeArgs& a, cudaStream_t st) {
+  using C = TreeScan<SKP, SVP>;
+  const cudaError_t e = ensure_smem_limit(tree_scan_kernel<SKP, SVP>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_scan_kernel<SKP, SVP>, dim3(a.grid), dim3(C::THREADS), C::SMEM, st, a);
+}
+
+template <int SKP>
+static cudaError_t launch_tree_scan_v(const TreeArgs& a, int SVP, cudaStream_t st) {
+  switch (SVP) {
+    case 1: return launch_tree_scan<SKP, 1>(a, st);
+    case 2: return launch_tree_scan<SKP, 2>(a, st);
+    case 4: return launch_tree_scan<SKP, 4>(a, st);
+    default: return launch_tree_scan<SKP, 8>(a, st);
+  }
+}
+
+template <int D>
+static int launch_tree(const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
+  const size_t s1 = std::max(sizeof(QtSmem<D>), sizeof(TreeDenseSmem<D>));
+  const size_t s3 = sizeof(TreeContractSmem<D>);
+  static_assert(sizeof(QtSmem<D>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax, "fits");
+  if (ensure_smem_limit(tree_prepare_kernel<D>, s1) != cudaSuccess ||
+      ensure_smem_limit(tree_contract_kernel<D>, s3) != cudaSuccess)
+    return ZKV_ERR_CUDA;
+  const int64_t b1 = a.qt.blocks() + 1 + t.items;
+  tree_prepare_kernel<D><<<(unsigned)b1, kQtThreads, s1, st>>>(a);
+  ZKV_CHECK_LAUNCH();
+  cudaError_t e;
+  switch (t.SKP) {
+    case 1: e = launch_tree_scan_v<1>(a, t.SVP, st); break;
+    case 2: e = launch_tree_scan_v<2>(a, t.SVP, st); break;
+    case 4: e = launch_tree_scan_v<4>(a, t.SVP, st); break;
+    default: e = launch_tree_scan_v<8>(a, t.SVP, st); break;
+  }
+  if (e != cudaSuccess) return ZKV_ERR_CUDA;
+  const int64_t tiles = ((int64_t)a.B * a.NRG + 7) / 8;
+  if (launch_pdl(tree_contract_kernel<D>, dim3((unsigned)(tiles * a.Sv * kTreeHalves), a.Hkv), dim3(256),
+                 s3, st, a) != cudaSuccess)
+    return ZKV_ERR_CUDA;
+  const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
+  if (launch_pdl(tree_finish_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a) !=
+      cudaSuccess)
+    return ZKV_ERR_CUDA;
+  return ZKV_OK;
+}
+
+}  // namespace zkv
+
+using namespace zkv;
+
+extern "C" size_t zkv_tree_workspace_size(const zkv_tree_params* p) {
+  if (validate_tree_shapes(p) != ZKV_OK) return 0;
+  return tree_plan(p).total;
+}
+
+extern "C" int zkv_rvq_tree_attn(const zkv_tree_params* p, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const int v = validate_tree(p);
+  if (v != ZKV_OK) return v;
+  const TreePlan t = tree_plan(p);
+  if (!workspace || workspace_bytes < t.total || ((uintptr_t)workspace & 255))
+    return ZKV_ERR_WORKSPACE;
+  unsigned char* ws = reinterpret_cast<unsigned char*>(workspace);
+  const float scale = p->softmax_scale > 0.f ? p->softmax_scale : (float)(1.0 / std::sqrt((double)p->d));
+  TreeArgs a{};
+  a.B = p->B; a.N = p->N; a.G = p->Hq / p->Hkv; a.Hq = p->Hq; a.Hkv = p->Hkv;
+  a.Sk = p->Sk; a.Sv = p->Sv; a.R = t.R; a.RP = t.RP; a.NRG = t.NRG; a.grid = t.grid;
+  a.Tcap = p->Tcap; a.Wcap = p->Wcap; a.max_comp = p->max_comp_len;
+  a.n_draft = p->n_draft;
+  a.dk = reinterpret_cast<const __half*>(p->draft_k);
+  a.dv = reinterpret_cast<const __half*>(p->draft_v);
+  a.k_sb = p->k_sb; a.k_sn = p->k_sn; a.k_sh = p->k_sh;
+  a.v_sb = p->v_sb; a.v_sn = p->v_sn; a.v_sh = p->v_sh;
+  a.mask = p->mask; a.m_sb = p->m_sb; a.m_sn = p->m_sn;
+  a.k_codes = p->k_codes; a.v_codes = p->v_codes; a.comp_len = p->comp_len; a.Cv = p->v_codebooks;
+  a.win_k = reinterpret_cast<const __half*>(p->win_k);
+  a.win_v = reinterpret_cast<const __half*>(p->win_v);
+  a.win_len = p->win_len;
+  a.out = p->out; a.lse = p->lse; a.err = p->error_flag;
+  a.table = p->block_table; a.max_pages = p->max_pages; a.n_pages = p->n_pages;
+  a.pshift = p->block_table ? log2_pow2(p->page_tokens) : 0;
+  QueryTables& q = a.qt;
+  q.B = p->B; q.N = p->N; q.G = a.G; q.Hkv = p->Hkv; q.Sk = p->Sk; q.SKP = t.SKP; q.RG = kTreeRG;
+  q.R = t.R; q.RP = t.RP;
+  q.q = reinterpret_cast<const __half*>(p->q);
+  q.q_sb = p->q_sb; q.q_sn = p->q_sn; q.q_sh = p->q_sh;
+  q.n_query = p->n_draft; q.Ck = p->k_codebooks; q.k_smooth = p->k_smooth;
+  q.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  q.rot = 1.0 / std::sqrt((double)p->d);
+  q.lut = reinterpret_cast<float*>(ws + t.lut);
+  a.pre = reinterpret_cast<int64_t*>(ws + t.pre);
+  a.pw = reinterpret_cast<float*>(ws + t.pw);
+  a.pm = reinterpret_cast<float*>(ws + t.pm);
+  a.dm = reinterpret_cast<float*>(ws + t.dm);
+  a.dl = reinterpret_cast<float*>(ws + t.dl);
+  a.dout = reinterpret_cast<float*>(ws + t.dout);
+  a.parts = reinterpret_cast<float*>(ws + t.parts);
+  a.rm = reinterpret_cast<float*>(ws + t.rm);
+  a.rl = reinterpret_cast<float*>(ws + t.rl);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  switch (p->d) {
+    case 64: return launch_tree<64>(a, t, st);
+    case 128: return launch_tree<128>(a, t, st);
+    default: return launch_tree<256>(a, t, st);
+  }
+}

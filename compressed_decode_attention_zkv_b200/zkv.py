@@ -6,8 +6,10 @@ is no fallback path.
 
 Entry points (same names as the C ABI):
   fwht, rvq_encode, rvq_reconstruct, decode_workspace_size, rvq_decode_attn,
-  rvq_decode_attn_noalloc, rvq_append
-plus PreparedAppend / PreparedDecode (the same calls with their arguments marshalled once)
+  rvq_decode_attn_noalloc, rvq_append, tree_workspace_size, rvq_tree_attn, rvq_tree_commit,
+  weights_workspace_size, rvq_accumulate_weights, rvq_evict
+plus PreparedAppend / PreparedDecode / PreparedTreeAttn / PreparedTreeCommit / PreparedAccumulate /
+PreparedEvict (the same calls with their arguments marshalled once)
 and ``RVQKVCache``, a small owner of one layer's compressed cache built on them
 (prefill -> append -> attend, the append/attend cache interface of the VeloxQuant-MLX page).
 """
@@ -29,9 +31,11 @@ ZKV_DEVERR_WIN_LEN = 2
 ZKV_DEVERR_TIMEOUT = 4
 ZKV_DEVERR_PAGE = 8
 ZKV_DEVERR_SMEM = 16
+ZKV_DEVERR_DRAFT = 32
 ZKV_DTYPE_F16, ZKV_DTYPE_F32 = 0, 1
 CODEBOOK_SIZE = 256
 DECODE_SCRATCH_BYTES = 8 << 20   # ZKV_DECODE_SCRATCH_BYTES: the no-allocation decode's array
+EVICT_MAX_TOKENS = 393216        # ZKV_EVICT_MAX_TOKENS: the largest capacity that rvq_evict takes
 
 
 class ZkvError(RuntimeError):
@@ -127,6 +131,58 @@ class MergePeersParams(ctypes.Structure):
                 ("out", c_void_p), ("lse", c_void_p), ("error_flag", c_void_p)]
 
 
+_PAGED = [("block_table", c_void_p), ("page_tokens", c_int64), ("max_pages", c_int64),
+          ("n_pages", c_int64)]
+
+
+class TreeParams(ctypes.Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("Hq", c_int), ("Hkv", c_int), ("d", c_int),
+                ("Sk", c_int), ("Sv", c_int), ("Tcap", c_int64), ("Wcap", c_int64),
+                ("max_comp_len", c_int64), ("softmax_scale", c_float),
+                ("q", c_void_p), ("q_sb", c_int64), ("q_sn", c_int64), ("q_sh", c_int64),
+                ("draft_k", c_void_p), ("k_sb", c_int64), ("k_sn", c_int64), ("k_sh", c_int64),
+                ("draft_v", c_void_p), ("v_sb", c_int64), ("v_sn", c_int64), ("v_sh", c_int64),
+                ("mask", c_void_p), ("m_sb", c_int64), ("m_sn", c_int64),
+                ("n_draft", c_void_p), ("k_codes", c_void_p), ("v_codes", c_void_p),
+                ("comp_len", c_void_p), ("k_codebooks", c_void_p), ("v_codebooks", c_void_p),
+                ("win_k", c_void_p), ("win_v", c_void_p), ("win_len", c_void_p),
+                ("out", c_void_p), ("lse", c_void_p), ("error_flag", c_void_p),
+                ("k_smooth", c_void_p)] + _PAGED
+
+
+class TreeCommitParams(ctypes.Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("M", c_int), ("Hkv", c_int), ("d", c_int),
+                ("Sk", c_int), ("Sv", c_int), ("Tcap", c_int64), ("Wcap", c_int64),
+                ("draft_k", c_void_p), ("k_sb", c_int64), ("k_sn", c_int64), ("k_sh", c_int64),
+                ("draft_v", c_void_p), ("v_sb", c_int64), ("v_sn", c_int64), ("v_sh", c_int64),
+                ("path", c_void_p), ("n_accept", c_void_p), ("win_k", c_void_p),
+                ("win_v", c_void_p), ("win_len", c_void_p), ("win_head", c_void_p),
+                ("comp_len", c_void_p), ("k_codes", c_void_p), ("v_codes", c_void_p),
+                ("k_codebooks", c_void_p), ("v_codebooks", c_void_p), ("error_flag", c_void_p),
+                ("k_smooth", c_void_p)] + _PAGED
+
+
+class WeightsParams(ctypes.Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("Hq", c_int), ("Hkv", c_int), ("d", c_int),
+                ("Sk", c_int), ("Tcap", c_int64), ("max_comp_len", c_int64),
+                ("softmax_scale", c_float),
+                ("q", c_void_p), ("q_sb", c_int64), ("q_sn", c_int64), ("q_sh", c_int64),
+                ("lse", c_void_p), ("k_codes", c_void_p), ("comp_len", c_void_p),
+                ("k_codebooks", c_void_p), ("acc", c_void_p), ("error_flag", c_void_p),
+                ("k_smooth", c_void_p)] + _PAGED
+
+
+class EvictParams(ctypes.Structure):
+    _fields_ = [("B", c_int), ("Hkv", c_int), ("Sk", c_int), ("Sv", c_int), ("Tcap", c_int64),
+                ("Tcap_out", c_int64), ("keep", c_int64), ("recent", c_int64),
+                ("k_codes", c_void_p), ("v_codes", c_void_p), ("acc", c_void_p),
+                ("comp_len", c_void_p), ("k_out", c_void_p), ("v_out", c_void_p),
+                ("acc_out", c_void_p), ("len_out", c_void_p), ("kept", c_void_p),
+                ("error_flag", c_void_p)] + _PAGED + \
+               [("block_table_out", c_void_p), ("page_tokens_out", c_int64),
+                ("max_pages_out", c_int64), ("n_pages_out", c_int64)]
+
+
 _lib = None
 
 
@@ -170,6 +226,19 @@ def lib() -> ctypes.CDLL:
         L.zkv_rvq_serve_step.restype = c_int
         L.zkv_rvq_serve_step.argtypes = [POINTER(AppendParams), POINTER(DecodeParams), c_void_p,
                                          c_size_t, c_void_p]
+        L.zkv_tree_workspace_size.restype = c_size_t
+        L.zkv_tree_workspace_size.argtypes = [POINTER(TreeParams)]
+        L.zkv_rvq_tree_attn.restype = c_int
+        L.zkv_rvq_tree_attn.argtypes = [POINTER(TreeParams), c_void_p, c_size_t, c_void_p]
+        L.zkv_rvq_tree_commit.restype = c_int
+        L.zkv_rvq_tree_commit.argtypes = [POINTER(TreeCommitParams), c_void_p]
+        L.zkv_weights_workspace_size.restype = c_size_t
+        L.zkv_weights_workspace_size.argtypes = [POINTER(WeightsParams)]
+        L.zkv_rvq_accumulate_weights.restype = c_int
+        L.zkv_rvq_accumulate_weights.argtypes = [POINTER(WeightsParams), c_void_p, c_size_t,
+                                                 c_void_p]
+        L.zkv_rvq_evict.restype = c_int
+        L.zkv_rvq_evict.argtypes = [POINTER(EvictParams), c_void_p]
         _lib = L
     return _lib
 
@@ -588,6 +657,406 @@ class PreparedDecode:
 
 
 # --------------------------------------------------------------------------------------------
+# Speculated continuations: tree attention and path commit
+# --------------------------------------------------------------------------------------------
+
+def _shape(t: torch.Tensor, name: str, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _one_device(**tensors):
+    """Every tensor lies on the current CUDA device (whose current stream the call uses)."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _rows(t: torch.Tensor, name: str, shape):
+    """fp16 [B, N, H, d] view (d contiguous, other strides multiples of 8): its three strides."""
+    _need(t, name, torch.float16, contiguous=False)
+    _shape(t, name, shape)
+    if t.stride(3) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    # the stride of an axis of one entry is never used
+    return [s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape[:3])]
+
+
+def _codes_of(k_codes, v_codes, block_table, B):
+    """(Hkv, Tcap, Sk, Sv, paged fields) after checks of the code arrays and their table."""
+    _need(k_codes, "k_codes", torch.uint8)
+    _need(v_codes, "v_codes", torch.uint8)
+    if k_codes.dim() != 4 or v_codes.dim() != 4:
+        raise ValueError("codes must be [B, Hkv, Tcap, S] or pools [n_pages, Hkv, P, S]")
+    _shape(v_codes[..., 0], "v_codes[..., 0]", k_codes.shape[:3])
+    if block_table is not None and block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    Hkv, Tcap, Sk, paged = _code_layout(k_codes, block_table)
+    rows = k_codes if block_table is None else block_table
+    if rows.shape[0] != B:
+        raise ValueError(f"the cache holds {rows.shape[0]} sequences, the call has {B}")
+    return Hkv, Tcap, Sk, v_codes.shape[3], paged
+
+
+def _books(books, name, Hkv, S, d):
+    _need(books, name, torch.float32)
+    _shape(books, name, (Hkv, S, CODEBOOK_SIZE, d))
+
+
+def _per_sequence(B, **lengths):
+    for name, t in lengths.items():
+        if t is not None:
+            _need(t, name, torch.int32)
+            _shape(t, name, (B,))
+
+
+def _flag(error_flag):
+    if error_flag is not None:
+        _need(error_flag, "error_flag", torch.int32)
+        if error_flag.numel() < 1:
+            raise ValueError("error_flag must hold one word")
+    return _ptr(error_flag)
+
+
+def _tree_params(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks, v_codebooks,
+                 win_k, win_v, win_len, mask, n_draft, out, lse, max_comp_len, softmax_scale,
+                 error_flag, k_smooth, block_table) -> TreeParams:
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, d]")
+    B, N, Hq, d = q.shape
+    Hkv, Tcap, Sk, Sv, paged = _codes_of(k_codes, v_codes, block_table, B)
+    qs = _rows(q, "q", (B, N, Hq, d))
+    ks = _rows(draft_k, "draft_k", (B, N, Hkv, d))
+    vs = _rows(draft_v, "draft_v", (B, N, Hkv, d))
+    _books(k_codebooks, "k_codebooks", Hkv, Sk, d)
+    _books(v_codebooks, "v_codebooks", Hkv, Sv, d)
+    _need(win_k, "win_k", torch.float16)
+    _need(win_v, "win_v", torch.float16)
+    if win_k.dim() != 4:
+        raise ValueError("win_k must be [B, Hkv, Wcap, d]")
+    Wcap = win_k.shape[2]
+    _shape(win_k, "win_k", (B, Hkv, Wcap, d))
+    _shape(win_v, "win_v", (B, Hkv, Wcap, d))
+    _per_sequence(B, comp_len=comp_len, win_len=win_len, n_draft=n_draft)
+    m_sb = m_sn = 0
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("mask must be bool or uint8")
+        _need(mask, "mask", mask.dtype, contiguous=False)
+        if mask.dim() == 2:
+            mask = mask[None]
+        if mask.dim() != 3 or mask.shape[0] not in (1, B) or tuple(mask.shape[1:]) != (N, N):
+            raise ValueError(f"mask must be [N, N] or [B, N, N] with N = {N}")
+        if N > 1 and mask.stride(2) != 1:
+            raise ValueError("mask rows must be contiguous")
+        m_sb = mask.stride(0) if mask.shape[0] > 1 else 0
+        m_sn = mask.stride(1) if N > 1 else 0
+    if out is not None:
+        _need(out, "out", torch.float32)
+        _shape(out, "out", (B, N, Hq, d))
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        _shape(lse, "lse", (B, N, Hq))
+    _one_device(q=q, draft_k=draft_k, draft_v=draft_v, k_codes=k_codes, v_codes=v_codes,
+                comp_len=comp_len, k_codebooks=k_codebooks, v_codebooks=v_codebooks, win_k=win_k,
+                win_v=win_v, win_len=win_len, mask=mask, n_draft=n_draft, out=out, lse=lse,
+                error_flag=error_flag, k_smooth=k_smooth, block_table=block_table)
+    return TreeParams(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, Sk=Sk, Sv=Sv, Tcap=Tcap, Wcap=Wcap,
+                      max_comp_len=Tcap if max_comp_len is None else int(max_comp_len),
+                      softmax_scale=0.0 if softmax_scale is None else float(softmax_scale),
+                      q=_ptr(q), q_sb=qs[0], q_sn=qs[1], q_sh=qs[2],
+                      draft_k=_ptr(draft_k), k_sb=ks[0], k_sn=ks[1], k_sh=ks[2],
+                      draft_v=_ptr(draft_v), v_sb=vs[0], v_sn=vs[1], v_sh=vs[2],
+                      mask=_ptr(mask), m_sb=m_sb, m_sn=m_sn, n_draft=_ptr(n_draft),
+                      k_codes=_ptr(k_codes), v_codes=_ptr(v_codes), comp_len=_ptr(comp_len),
+                      k_codebooks=_ptr(k_codebooks), v_codebooks=_ptr(v_codebooks),
+                      win_k=_ptr(win_k), win_v=_ptr(win_v), win_len=_ptr(win_len),
+                      out=_ptr(out), lse=_ptr(lse), error_flag=_flag(error_flag),
+                      k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged)
+
+
+def tree_workspace_size(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks,
+                        v_codebooks, win_k, win_v, win_len, max_comp_len=None,
+                        block_table=None) -> int:
+    """Bytes of device workspace that rvq_tree_attn needs for these shapes."""
+    p = _tree_params(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks, v_codebooks,
+                     win_k, win_v, win_len, None, None, None, None, max_comp_len, None, None,
+                     None, block_table)
+    return _workspace_need("zkv_tree_workspace_size", lib().zkv_tree_workspace_size, p)
+
+
+def _workspace_need(name, fn, p) -> int:
+    n = fn(ctypes.byref(p))
+    if n == 0:
+        raise ZkvError(name, ZKV_ERR_INVALID_ARG, "shapes invalid or unsupported")
+    return n
+
+
+def _workspace(name, need, workspace, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8)
+    _one_device(workspace=workspace)
+    if workspace.numel() < need:
+        raise ZkvError(name, ZKV_ERR_WORKSPACE,
+                       f"workspace holds {workspace.numel()} bytes, {need} needed")
+    return workspace
+
+
+class _Prepared:
+    """A library call with its arguments validated and marshalled once, on one device."""
+
+    def _set(self, name, p, workspace, *keep):
+        self._name, self._p, self._keep = name, p, keep + (workspace,)
+        self._fn = getattr(lib(), name)
+        self._args = (ctypes.byref(p),) if workspace is None else \
+            (ctypes.byref(p), c_void_p(workspace.data_ptr()), c_size_t(workspace.numel()))
+        self._device = torch.cuda.current_device()
+
+    def __call__(self):
+        st = self._fn(*self._args, torch.cuda.current_stream(self._device).cuda_stream)
+        if st != ZKV_OK:
+            raise ZkvError(self._name, st)
+
+
+class PreparedTreeAttn(_Prepared):
+    """rvq_tree_attn with its arguments validated and marshalled once (workspace included).  The
+    tensors must keep their storage; max_comp_len must stay an upper bound of every comp_len for
+    as long as the object is used.  Calling it runs one verification step on the current stream
+    and returns (out, lse); rows behind a sequence's drafts keep what they held (zeros in arrays
+    that the object makes)."""
+
+    def __init__(self, q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks, v_codebooks,
+                 win_k, win_v, win_len, mask=None, n_draft=None, out=None, lse=None,
+                 max_comp_len=None, softmax_scale=None, workspace: torch.Tensor | None = None,
+                 error_flag=None, k_smooth=None, block_table=None):
+        p = _tree_params(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks,
+                         v_codebooks, win_k, win_v, win_len, mask, n_draft, out, lse,
+                         max_comp_len, softmax_scale, error_flag, k_smooth, block_table)
+        if out is None:
+            out = torch.zeros(tuple(q.shape), dtype=torch.float32, device=q.device)
+            p.out = _ptr(out)
+        if lse is None:
+            lse = torch.zeros(tuple(q.shape[:3]), dtype=torch.float32, device=q.device)
+            p.lse = _ptr(lse)
+        need = _workspace_need("zkv_rvq_tree_attn", lib().zkv_tree_workspace_size, p)
+        workspace = _workspace("zkv_rvq_tree_attn", need, workspace, q.device)
+        self.out, self.lse = out, lse
+        self._set("zkv_rvq_tree_attn", p, workspace, q, draft_k, draft_v, k_codes, v_codes,
+                  comp_len, k_codebooks, v_codebooks, win_k, win_v, win_len, mask, n_draft, out,
+                  lse, error_flag, k_smooth, block_table)
+
+    def __call__(self):
+        super().__call__()
+        return self.out, self.lse
+
+
+def rvq_tree_attn(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks, v_codebooks,
+                  win_k, win_v, win_len, mask=None, n_draft=None, out=None, lse=None,
+                  max_comp_len=None, softmax_scale=None, workspace=None, error_flag=None,
+                  k_smooth=None, block_table=None):
+    """Attention of a tree of drafted tokens over the cache (see include/zkv.h): the verification
+    step of speculative decoding.  q fp16 [B, N, Hq, d], draft_k / draft_v fp16 [B, N, Hkv, d]
+    (views allowed, d contiguous); mask bool or uint8 [N, N] or [B, N, N], mask[b, i, j] != 0
+    where draft i attends to draft j (None: a chain, j <= i); n_draft int32 [B] (None: N
+    everywhere); the cache as in rvq_decode_attn.
+    Returns (out float32 [B, N, Hq, d], lse float32 [B, N, Hq])."""
+    return PreparedTreeAttn(q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks,
+                            v_codebooks, win_k, win_v, win_len, mask, n_draft, out, lse,
+                            max_comp_len, softmax_scale, workspace, error_flag, k_smooth,
+                            block_table)()
+
+
+class PreparedTreeCommit(_Prepared):
+    """rvq_tree_commit with its arguments validated and marshalled once.  The tensors must keep
+    their storage (their contents may change between calls)."""
+
+    def __init__(self, draft_k, draft_v, path, n_accept, win_k, win_v, win_len, win_head,
+                 comp_len, k_codes, v_codes, k_codebooks, v_codebooks, error_flag=None,
+                 k_smooth=None, block_table=None):
+        if draft_k.dim() != 4:
+            raise ValueError("draft_k must be [B, N, Hkv, d]")
+        B, N, _, d = draft_k.shape
+        Hkv, Tcap, Sk, Sv, paged = _codes_of(k_codes, v_codes, block_table, B)
+        ks = _rows(draft_k, "draft_k", (B, N, Hkv, d))
+        vs = _rows(draft_v, "draft_v", (B, N, Hkv, d))
+        _need(path, "path", torch.int32)
+        if path.dim() != 2 or path.shape[0] != B:
+            raise ValueError(f"path must be [B = {B}, M], got {list(path.shape)}")
+        _need(win_k, "win_k", torch.float16)
+        _need(win_v, "win_v", torch.float16)
+        if win_k.dim() != 4:
+            raise ValueError("win_k must be [B, Hkv, Wcap, d]")
+        _shape(win_k, "win_k", (B, Hkv, win_k.shape[2], d))
+        _shape(win_v, "win_v", win_k.shape)
+        _per_sequence(B, n_accept=n_accept, win_len=win_len, win_head=win_head, comp_len=comp_len)
+        _books(k_codebooks, "k_codebooks", Hkv, Sk, d)
+        _books(v_codebooks, "v_codebooks", Hkv, Sv, d)
+        _one_device(draft_k=draft_k, draft_v=draft_v, path=path, n_accept=n_accept, win_k=win_k,
+                    win_v=win_v, win_len=win_len, win_head=win_head, comp_len=comp_len,
+                    k_codes=k_codes, v_codes=v_codes, k_codebooks=k_codebooks,
+                    v_codebooks=v_codebooks, error_flag=error_flag, k_smooth=k_smooth,
+                    block_table=block_table)
+        p = TreeCommitParams(B=B, N=N, M=path.shape[1], Hkv=Hkv, d=d, Sk=Sk, Sv=Sv, Tcap=Tcap,
+                             Wcap=win_k.shape[2], draft_k=_ptr(draft_k), k_sb=ks[0], k_sn=ks[1],
+                             k_sh=ks[2], draft_v=_ptr(draft_v), v_sb=vs[0], v_sn=vs[1],
+                             v_sh=vs[2], path=_ptr(path), n_accept=_ptr(n_accept),
+                             win_k=_ptr(win_k), win_v=_ptr(win_v), win_len=_ptr(win_len),
+                             win_head=_ptr(win_head), comp_len=_ptr(comp_len),
+                             k_codes=_ptr(k_codes), v_codes=_ptr(v_codes),
+                             k_codebooks=_ptr(k_codebooks), v_codebooks=_ptr(v_codebooks),
+                             error_flag=_flag(error_flag),
+                             k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged)
+        self._set("zkv_rvq_tree_commit", p, None, draft_k, draft_v, path, n_accept, win_k, win_v,
+                  win_len, win_head, comp_len, k_codes, v_codes, k_codebooks, v_codebooks,
+                  error_flag, k_smooth, block_table)
+
+
+def rvq_tree_commit(draft_k, draft_v, path, n_accept, win_k, win_v, win_len, win_head, comp_len,
+                    k_codes, v_codes, k_codebooks, v_codebooks, error_flag=None, k_smooth=None,
+                    block_table=None):
+    """The accepted drafts enter the cache (see include/zkv.h): sequence b appends the drafts
+    path[b, :n_accept[b]] in this order.  path int32 [B, M], n_accept int32 [B]; state updated in
+    place as by n_accept[b] calls of rvq_append for each sequence."""
+    PreparedTreeCommit(draft_k, draft_v, path, n_accept, win_k, win_v, win_len, win_head,
+                       comp_len, k_codes, v_codes, k_codebooks, v_codebooks, error_flag, k_smooth,
+                       block_table)()
+
+
+# --------------------------------------------------------------------------------------------
+# A cache within a budget: attention-weight totals and eviction
+# --------------------------------------------------------------------------------------------
+
+def _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len, softmax_scale,
+                    error_flag, k_smooth, block_table) -> WeightsParams:
+    if q.dim() == 3:
+        q = q[:, None]
+    if lse.dim() == 2:
+        lse = lse[:, None]
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, d] or [B, Hq, d]")
+    B, N, Hq, d = q.shape
+    Hkv, Tcap, Sk, _, paged = _codes_of(k_codes, k_codes, block_table, B)
+    qs = _rows(q, "q", (B, N, Hq, d))
+    _need(lse, "lse", torch.float32)
+    _shape(lse, "lse", (B, N, Hq))
+    _per_sequence(B, comp_len=comp_len)
+    _books(k_codebooks, "k_codebooks", Hkv, Sk, d)
+    _need(acc, "acc", torch.float32)
+    _shape(acc, "acc", (B, Hkv, Tcap))
+    _one_device(q=q, lse=lse, k_codes=k_codes, comp_len=comp_len, k_codebooks=k_codebooks,
+                acc=acc, error_flag=error_flag, k_smooth=k_smooth, block_table=block_table)
+    return WeightsParams(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, Sk=Sk, Tcap=Tcap,
+                         max_comp_len=Tcap if max_comp_len is None else int(max_comp_len),
+                         softmax_scale=0.0 if softmax_scale is None else float(softmax_scale),
+                         q=_ptr(q), q_sb=qs[0], q_sn=qs[1], q_sh=qs[2], lse=_ptr(lse),
+                         k_codes=_ptr(k_codes), comp_len=_ptr(comp_len),
+                         k_codebooks=_ptr(k_codebooks), acc=_ptr(acc),
+                         error_flag=_flag(error_flag),
+                         k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged)
+
+
+def weights_workspace_size(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len=None,
+                           block_table=None) -> int:
+    """Bytes of device workspace that rvq_accumulate_weights needs for these shapes."""
+    p = _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len, None, None,
+                        None, block_table)
+    return _workspace_need("zkv_weights_workspace_size", lib().zkv_weights_workspace_size, p)
+
+
+class PreparedAccumulate(_Prepared):
+    """rvq_accumulate_weights with its arguments validated and marshalled once (workspace
+    included).  The tensors must keep their storage; max_comp_len must stay an upper bound of
+    every comp_len for as long as the object is used.  Calling it returns acc."""
+
+    def __init__(self, q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len=None,
+                 softmax_scale=None, workspace: torch.Tensor | None = None, error_flag=None,
+                 k_smooth=None, block_table=None):
+        p = _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len,
+                            softmax_scale, error_flag, k_smooth, block_table)
+        need = _workspace_need("zkv_rvq_accumulate_weights", lib().zkv_weights_workspace_size, p)
+        workspace = _workspace("zkv_rvq_accumulate_weights", need, workspace, q.device)
+        self.acc = acc
+        self._set("zkv_rvq_accumulate_weights", p, workspace, q, lse, k_codes, comp_len,
+                  k_codebooks, acc, error_flag, k_smooth, block_table)
+
+    def __call__(self):
+        super().__call__()
+        return self.acc
+
+
+def rvq_accumulate_weights(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len=None,
+                           softmax_scale=None, workspace=None, error_flag=None, k_smooth=None,
+                           block_table=None):
+    """acc[b, kvh, t] += the attention weight that compressed token t received from the queries
+    (see include/zkv.h).  q fp16 [B, N, Hq, d] (or [B, Hq, d]: one query each) and lse float32
+    [B, N, Hq] (or [B, Hq]) as rvq_tree_attn / rvq_decode_attn took and gave them; acc float32
+    [B, Hkv, Tcap].  A query whose lse is infinite or NaN adds nothing.  Returns acc."""
+    return PreparedAccumulate(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len,
+                              softmax_scale, workspace, error_flag, k_smooth, block_table)()
+
+
+class PreparedEvict(_Prepared):
+    """rvq_evict with its arguments validated and marshalled once.  The tensors must keep their
+    storage (their contents may change between calls)."""
+
+    def __init__(self, k_codes, v_codes, comp_len, acc, keep, recent=0, k_out=None, v_out=None,
+                 len_out=None, acc_out=None, kept=None, error_flag=None, block_table=None,
+                 block_table_out=None):
+        B = comp_len.shape[0]
+        Hkv, Tcap, Sk, Sv, paged = _codes_of(k_codes, v_codes, block_table, B)
+        if (k_out is None) != (v_out is None):
+            raise ValueError("k_out and v_out go together")
+        if k_out is None:
+            if block_table_out is not None:
+                raise ValueError("block_table_out needs k_out and v_out")
+            k_out, v_out, block_table_out = k_codes, v_codes, block_table
+        if len_out is None:
+            len_out = comp_len
+        Hout, Tout, Sko, Svo, out = _codes_of(k_out, v_out, block_table_out, B)
+        if (Hout, Sko, Svo) != (Hkv, Sk, Sv):
+            raise ValueError("k_out and v_out must have the heads and stages of k_codes and v_codes")
+        _need(acc, "acc", torch.float32)
+        _shape(acc, "acc", (B, Hkv, Tcap))
+        if acc_out is None:
+            if Tout != Tcap:
+                raise ValueError("acc_out is needed where the destination's capacity differs")
+            acc_out = acc
+        _need(acc_out, "acc_out", torch.float32)
+        _shape(acc_out, "acc_out", (B, Hkv, Tout))
+        _per_sequence(B, comp_len=comp_len, len_out=len_out)
+        keep, recent = int(keep), int(recent)
+        if kept is not None:
+            _need(kept, "kept", torch.int32)
+            _shape(kept, "kept", (B, Hkv, keep))
+        _one_device(k_codes=k_codes, v_codes=v_codes, comp_len=comp_len, acc=acc, k_out=k_out,
+                    v_out=v_out, len_out=len_out, acc_out=acc_out, kept=kept,
+                    error_flag=error_flag, block_table=block_table,
+                    block_table_out=block_table_out)
+        p = EvictParams(B=B, Hkv=Hkv, Sk=Sk, Sv=Sv, Tcap=Tcap, Tcap_out=Tout, keep=keep,
+                        recent=recent, k_codes=_ptr(k_codes), v_codes=_ptr(v_codes),
+                        acc=_ptr(acc), comp_len=_ptr(comp_len), k_out=_ptr(k_out),
+                        v_out=_ptr(v_out), acc_out=_ptr(acc_out), len_out=_ptr(len_out),
+                        kept=_ptr(kept), error_flag=_flag(error_flag),
+                        **paged, **{n + "_out": v for n, v in out.items()})
+        self._set("zkv_rvq_evict", p, None, k_codes, v_codes, comp_len, acc, k_out, v_out,
+                  len_out, acc_out, kept, error_flag, block_table, block_table_out)
+
+
+def rvq_evict(k_codes, v_codes, comp_len, acc, keep, recent=0, k_out=None, v_out=None,
+              len_out=None, acc_out=None, kept=None, error_flag=None, block_table=None,
+              block_table_out=None):
+    """Shrinks every sequence's compressed prefix to at most ``keep`` tokens: the ``recent`` newest
+    and the older ones with the largest totals acc (see include/zkv.h).  In place unless other
+    arrays are given (k_out with v_out, acc_out, len_out; block_table_out for a paged
+    destination).  kept: optional int32 [B, Hkv, keep], the source position of each kept token (-1
+    behind them).  Capacity at most EVICT_MAX_TOKENS."""
+    PreparedEvict(k_codes, v_codes, comp_len, acc, keep, recent, k_out, v_out, len_out, acc_out,
+                  kept, error_flag, block_table, block_table_out)()
+
+
+# --------------------------------------------------------------------------------------------
 # A layer's compressed cache
 # --------------------------------------------------------------------------------------------
 
@@ -788,7 +1257,10 @@ class RVQKVCache:
     """Compressed KV cache of one attention layer: RVQ codes for old tokens, an fp16 window for
     the newest ones.  prefill() encodes a prompt, append() inserts one token per sequence
     (evicting and encoding the oldest window token when the window is full), attend() runs one
-    decode step of attention, step() does both in one library call.  All state lives on the GPU; lengths never leave the device.
+    decode step of attention, step() does both in one library call.  verify() attends with a tree
+    of drafted tokens and commit() inserts the accepted ones; note_weights() adds up the attention
+    that each compressed token receives (in ``acc``, made by its first call) and evict() keeps the
+    heaviest.  All state lives on the GPU; lengths never leave the device.
     k_smooth: optional float32 [Hkv, d] key smoothing factors (the key codebooks must have been
     trained on smoothed keys)."""
 
@@ -811,6 +1283,7 @@ class RVQKVCache:
         self.win_head = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_comp_len = 0      # host-side bound used to size decode launches
+        self.acc = None            # float32 [batch, Hkv, Tcap] attention-weight totals
         self._ws = None
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
@@ -833,6 +1306,8 @@ class RVQKVCache:
         self.win_len.fill_(W)
         self.win_head.zero_()
         self.max_comp_len = Tc
+        if self.acc is not None:
+            self.acc.zero_()
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor):
         """k_new, v_new: fp16 [B, Hkv, d]."""
@@ -869,6 +1344,55 @@ class RVQKVCache:
                               max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
                               workspace=self._ws, error_flag=self.error_flag,
                               k_smooth=self.k_smooth)
+
+    def _scratch(self, need: int) -> torch.Tensor:
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
+        return self._ws
+
+    def verify(self, q: torch.Tensor, draft_k: torch.Tensor, draft_v: torch.Tensor, mask=None,
+               n_draft=None, softmax_scale=None, out=None, lse=None):
+        """Attention of N drafted tokens per sequence over the cache and over each other, which
+        leaves the cache as it is (rvq_tree_attn).  q fp16 [B, N, Hq, d], draft_k / draft_v fp16
+        [B, N, Hkv, d] -> (out float32 [B, N, Hq, d], lse float32 [B, N, Hq])."""
+        args = (q, draft_k, draft_v, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv,
+                self.win_k, self.win_v, self.win_len)
+        need = tree_workspace_size(*args, max_comp_len=self.max_comp_len)
+        return rvq_tree_attn(*args, mask=mask, n_draft=n_draft, out=out, lse=lse,
+                             max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
+                             workspace=self._scratch(need), error_flag=self.error_flag,
+                             k_smooth=self.k_smooth)
+
+    def commit(self, draft_k: torch.Tensor, draft_v: torch.Tensor, path: torch.Tensor,
+               n_accept: torch.Tensor):
+        """The drafts path[b, :n_accept[b]] enter the cache of sequence b (rvq_tree_commit).
+        path int32 [B, M], n_accept int32 [B]."""
+        rvq_tree_commit(draft_k, draft_v, path, n_accept, self.win_k, self.win_v, self.win_len,
+                        self.win_head, self.comp_len, self.k_codes, self.v_codes, self.Ck, self.Cv,
+                        self.error_flag, self.k_smooth)
+        self.max_comp_len = min(self.max_comp_len + path.shape[1], self.Tcap)
+
+    def note_weights(self, q: torch.Tensor, lse: torch.Tensor, softmax_scale=None):
+        """Adds the attention weight of q over the compressed tokens to ``acc``
+        (rvq_accumulate_weights).  q and lse as attend() or verify() took and gave them, before
+        any token was appended in between."""
+        if self.acc is None:
+            self.acc = torch.zeros(self.k_codes.shape[:3], dtype=torch.float32,
+                                   device=self.k_codes.device)
+        args = (q, lse, self.k_codes, self.comp_len, self.Ck, self.acc)
+        need = weights_workspace_size(*args, max_comp_len=self.max_comp_len)
+        return rvq_accumulate_weights(*args, max_comp_len=self.max_comp_len,
+                                      softmax_scale=softmax_scale, workspace=self._scratch(need),
+                                      error_flag=self.error_flag, k_smooth=self.k_smooth)
+
+    def evict(self, keep: int, recent: int = 0, kept=None):
+        """Keeps at most ``keep`` compressed tokens per sequence and kv head: the ``recent`` newest
+        and those with the largest totals in ``acc`` (rvq_evict, in place)."""
+        if self.acc is None:
+            raise ValueError("evict() needs the totals that note_weights() makes")
+        rvq_evict(self.k_codes, self.v_codes, self.comp_len, self.acc, keep, recent, kept=kept,
+                  error_flag=self.error_flag)
+        self.max_comp_len = min(self.max_comp_len, int(keep))
 
     def memory_bytes(self) -> int:
         """Bytes held by codes and window (codebooks are shared across layers' caches)."""

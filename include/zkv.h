@@ -61,6 +61,8 @@ typedef enum {
                                    0 (decode) / the append writes nothing for that sequence      */
 #define ZKV_DEVERR_SMEM 16      /* the decode scan's shared-memory layout did not fit the CTA's
                                    shared window (its partial results are absent)               */
+#define ZKV_DEVERR_DRAFT 32     /* n_draft[b] outside 0..N (clamped); n_accept[b] outside 0..M or a
+                                   path entry outside 0..N-1 (that sequence commits nothing)     */
 
 #define ZKV_DTYPE_F16 0
 #define ZKV_DTYPE_F32 1
@@ -71,8 +73,9 @@ typedef enum {
 const char* zkv_status_string(int status);
 
 /* Library ABI version (major * 100 + minor): 1.01 adds the serving step, the paged layout,
- * key smoothing, product VQ and the context-parallel combines to 1.00's encode / decode. */
-#define ZKV_VERSION 101
+ * key smoothing, product VQ and the context-parallel combines to 1.00's encode / decode; 1.02
+ * the tree attention, the path commit, the attention-weight totals and the eviction. */
+#define ZKV_VERSION 102
 int zkv_version(void);
 
 /*
@@ -493,6 +496,196 @@ typedef struct {
 } zkv_lse_merge_peers_params;
 
 int zkv_lse_merge_peers(const zkv_lse_merge_peers_params* p, void* stream);
+
+/*
+ * zkv_rvq_tree_attn -- attention of a tree of drafted tokens over the cache: the verification
+ * step of speculative decoding.  Sequence b has n_draft[b] <= N drafted tokens, each with its
+ * own queries, key and value; every draft attends to the sequence's compressed prefix, to its
+ * fp16 window and to those drafts that the mask names.
+ * Passages: as zkv_rvq_decode_attn (one query token per sequence there, N here); the tree of
+ * drafts has no counterpart on the pages.
+ * Computes, for b < B, i < n_draft[b], h < Hq, kvh = h / (Hq/Hkv):
+ *   keys = compressed prefix (comp_len[b] tokens, as zkv_rvq_decode_attn)
+ *          U { win_k[b][kvh][w] : w < win_len[b] }
+ *          U { draft_k[b][j][kvh] : j < n_draft[b], mask[b][i][j] != 0 }      (values likewise)
+ *   out[b][i][h] = softmax(softmax_scale * q[b][i][h] . keys) . values         (float32)
+ *   lse[b][i][h] = natural log of sum exp(softmax_scale * q . k)              (float32, or NULL)
+ * A row without any key gives out = 0 and lse = -inf.  Rows i >= n_draft[b] of out and lse are
+ * not written.  Results do not depend on the order in which thread blocks run.
+ * Layouts (strides in elements; the last index, d or j, is contiguous):
+ *   q        fp16, (b, i, h) at q + b*q_sb + i*q_sn + h*q_sh
+ *   draft_k, draft_v fp16, (b, i, kvh) at x + b*k_sb + i*k_sn + kvh*k_sh (v_sb, ... for values)
+ *   mask     uint8, (b, i, j) at mask + b*m_sb + i*m_sn + j; m_sb = 0 shares one tree among
+ *            the sequences; NULL: a chain, j <= i
+ *   n_draft  int32 [B] (device) or NULL (every sequence has N drafts)
+ *   out      float32 [B][N][Hq][d] contiguous; lse float32 [B][N][Hq] contiguous
+ *   the cache, its codebooks, k_smooth and the paged layout: as zkv_decode_params
+ * 1 <= N <= 256; q, draft_k and draft_v rows 16-byte aligned (base and strides multiples of 8).
+ * Scores are float32 sums of float32 table entries; weights are accumulated as integers whose
+ * unit is 2^-29 of a scan tile's total or finer, and the output is normalised by their sum.
+ * Workspace: zkv_tree_workspace_size(p) bytes, 256-byte aligned, no initial contents; it must
+ *   not be shared by calls that run concurrently (two captured graphs replayed at once
+ *   included).  It grows with B * Hkv * N * Hq / Hkv.
+ * The first call on a device sets kernel attributes; make it before stream capture.
+ * Errors: INVALID_ARG, UNSUPPORTED (d, S, N, Hq/Hkv > 8), WORKSPACE, CUDA.
+ */
+typedef struct {
+  int B, N, Hq, Hkv, d, Sk, Sv;
+  int64_t Tcap, Wcap, max_comp_len;
+  float softmax_scale;
+  const uint16_t* q;
+  int64_t q_sb, q_sn, q_sh;
+  const uint16_t* draft_k;
+  int64_t k_sb, k_sn, k_sh;
+  const uint16_t* draft_v;
+  int64_t v_sb, v_sn, v_sh;
+  const uint8_t* mask;
+  int64_t m_sb, m_sn;
+  const int32_t* n_draft;
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const int32_t* comp_len;
+  const float* k_codebooks;
+  const float* v_codebooks;
+  const uint16_t* win_k;
+  const uint16_t* win_v;
+  const int32_t* win_len;
+  float* out;
+  float* lse;
+  int32_t* error_flag;
+  const float* k_smooth;
+  const int32_t* block_table;
+  int64_t page_tokens, max_pages, n_pages;
+} zkv_tree_params;
+
+size_t zkv_tree_workspace_size(const zkv_tree_params* p);
+int zkv_rvq_tree_attn(const zkv_tree_params* p, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * zkv_rvq_tree_commit -- the accepted drafts enter the cache: sequence b takes n_accept[b] <= M
+ * tokens, the drafts path[b][0], path[b][1], ... in this order.
+ * Passages: as zkv_rvq_append.
+ * The result is that of n_accept[b] appends of one token each (zkv_rvq_append's window rule:
+ * free slots first, then the oldest token is evicted, encoded and appended to the prefix; a
+ * draft that is itself evicted in the same call is encoded too).  Every sequence counts for
+ * itself: n_accept[b] = 0 leaves it as it was.
+ * A sequence is left unchanged as a whole, with the named bit set, if n_accept[b] is outside
+ * 0..M or one of its path entries outside 0..N-1 (ZKV_DEVERR_DRAFT), if its window state is
+ * invalid (ZKV_DEVERR_WIN_LEN), if its evicted tokens do not fit Tcap (ZKV_DEVERR_COMP_LEN) or
+ * would go to a page outside the pool (ZKV_DEVERR_PAGE).
+ * Layouts: draft_k / draft_v as zkv_tree_params; path int32 [B][M]; n_accept int32 [B]; the
+ * state as zkv_append_params, updated in place.  Wcap >= 1, 1 <= N, 1 <= M <= 256.
+ * No workspace.  Errors: INVALID_ARG, UNSUPPORTED (d, S, M), CUDA.
+ */
+typedef struct {
+  int B, N, M, Hkv, d, Sk, Sv;
+  int64_t Tcap, Wcap;
+  const uint16_t* draft_k;
+  int64_t k_sb, k_sn, k_sh;
+  const uint16_t* draft_v;
+  int64_t v_sb, v_sn, v_sh;
+  const int32_t* path;
+  const int32_t* n_accept;
+  uint16_t* win_k;
+  uint16_t* win_v;
+  int32_t* win_len;
+  int32_t* win_head;
+  int32_t* comp_len;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  const float* k_codebooks;
+  const float* v_codebooks;
+  int32_t* error_flag;
+  const float* k_smooth;
+  const int32_t* block_table;
+  int64_t page_tokens, max_pages, n_pages;
+} zkv_tree_commit_params;
+
+int zkv_rvq_tree_commit(const zkv_tree_commit_params* p, void* stream);
+
+/*
+ * zkv_rvq_accumulate_weights -- adds to each compressed token the attention weight that it
+ * receives from N queries per sequence (N = 1: one decode step).
+ * Passages: zerokv-neo 4.0.0 (heavy_hitter_budget: tokens kept by the attention that they
+ * received); the key scores as zkv_rvq_decode_attn.
+ *   acc[b][kvh][t] += sum over i < N and the heads h of kvh of
+ *                     exp(softmax_scale * q[b][i][h] . k_t - lse[b][i][h]),  t < comp_len[b]
+ * lse is what the attention over the whole context gave (zkv_rvq_decode_attn,
+ * zkv_rvq_tree_attn), so each query hands out a total weight of one over the context.  A query
+ * whose lse is -inf (it attended to nothing), +inf or NaN adds nothing: set +inf for the rows
+ * that shall not count, such as rejected drafts.  Entries at t >= comp_len[b] are not touched.
+ * Layouts: q as zkv_tree_params; lse float32 [B][N][Hq] contiguous; acc float32
+ * [B][Hkv][Tcap] contiguous (by position in both code layouts); the rest as zkv_decode_params.
+ * Workspace: zkv_weights_workspace_size(p) bytes, 256-byte aligned, as zkv_rvq_tree_attn's.
+ * Errors: INVALID_ARG, UNSUPPORTED (d, S, N > 256, Hq/Hkv > 8), WORKSPACE, CUDA.
+ */
+typedef struct {
+  int B, N, Hq, Hkv, d, Sk;
+  int64_t Tcap, max_comp_len;
+  float softmax_scale;
+  const uint16_t* q;
+  int64_t q_sb, q_sn, q_sh;
+  const float* lse;
+  const uint8_t* k_codes;
+  const int32_t* comp_len;
+  const float* k_codebooks;
+  float* acc;
+  int32_t* error_flag;
+  const float* k_smooth;
+  const int32_t* block_table;
+  int64_t page_tokens, max_pages, n_pages;
+} zkv_weights_params;
+
+size_t zkv_weights_workspace_size(const zkv_weights_params* p);
+int zkv_rvq_accumulate_weights(const zkv_weights_params* p, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * zkv_rvq_evict -- shrinks the compressed prefix of every sequence to at most `keep` tokens:
+ * the `recent` newest ones and, of the older ones, those with the largest totals.
+ * Passages: zerokv-neo 4.0.0 (heavy_hitter_budget).
+ * Per (b, kvh), with n = comp_len[b] (clamped to 0..Tcap), m = min(n, keep):
+ *   n <= keep: every token is kept.  Otherwise tokens t >= n - recent are kept, and the
+ *   keep - recent of the others whose acc[b][kvh][t] is largest (equal totals: the lower t
+ *   first; a NaN counts as smaller than any number; -0 equals +0).
+ *   The kept tokens move, in their order, to positions 0..m-1 of the destination: codes, and
+ *   their totals unchanged.  acc_out[m..n) (as far as it exists) becomes 0, so that tokens
+ *   appended there start without a total.  kept[b][kvh][j] is the source position of the
+ *   token now at j (-1 for j >= m).  len_out[b] = m.  Code rows at m and behind are left as
+ *   they were.
+ * The kv heads of a sequence choose for themselves; the length is the same for all.
+ * In place: k_out == k_codes, v_out == v_codes, acc_out == acc and len_out == comp_len, with
+ * the same capacity and block table (any of the four may instead be a separate buffer; partial
+ * overlap is not allowed).  An in-place call on pages that two sequences share is an error of
+ * the caller: evict to pages of their own.
+ * Layouts: codes as zkv_decode_params, source and destination each contiguous or paged (its
+ * own table and pool); acc float32 [B][Hkv][Tcap], acc_out float32 [B][Hkv][Tcap_out]; kept
+ * int32 [B][Hkv][keep] or NULL.  0 <= recent <= keep, 1 <= keep <= Tcap_out.  A bad page of the
+ * source reads as code 0, a row of a bad destination page is not written (ZKV_DEVERR_PAGE).
+ * No workspace.  Errors: INVALID_ARG, UNSUPPORTED (S, Tcap > ZKV_EVICT_MAX_TOKENS), CUDA.
+ */
+#define ZKV_EVICT_MAX_TOKENS 393216
+typedef struct {
+  int B, Hkv, Sk, Sv;
+  int64_t Tcap, Tcap_out, keep, recent;
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* acc;
+  const int32_t* comp_len;
+  uint8_t* k_out;
+  uint8_t* v_out;
+  float* acc_out;
+  int32_t* len_out;
+  int32_t* kept;
+  int32_t* error_flag;
+  const int32_t* block_table;
+  int64_t page_tokens, max_pages, n_pages;
+  const int32_t* block_table_out;
+  int64_t page_tokens_out, max_pages_out, n_pages_out;
+} zkv_evict_params;
+
+int zkv_rvq_evict(const zkv_evict_params* p, void* stream);
 
 #ifdef __cplusplus
 }
