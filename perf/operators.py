@@ -436,9 +436,11 @@ def _step(s):
     if "step" not in s:
         from compressed_decode_attention_zkv_b200 import zkv
         c = s["case"]
+        for x in ("k_codes", "v_codes"):     # the package takes pools whose pages lie one by one
+            s[x + "_pool"] = s[x].contiguous() if x in s else None
         if c["op"] == "tree":
             s["step"] = zkv.PreparedTreeAttn(
-                s["q"], s["draft_k"], s["draft_v"], s["k_codes"], s["v_codes"], s["comp_len"], s["Ck"],
+                s["q"], s["draft_k"], s["draft_v"], s["k_codes_pool"], s["v_codes_pool"], s["comp_len"], s["Ck"],
                 s["Cv"], s["win_k"], s["win_v"], s["win_len"], mask=s["mask"], n_draft=s["n_draft"],
                 out=s["out"], lse=s["lse"], max_comp_len=c["T"], block_table=s["table"])
         elif c["op"] == "commit":
@@ -448,7 +450,7 @@ def _step(s):
                 comp, s["k_codes"], s["v_codes"], s["Ck"], s["Cv"])
         elif c["op"] == "weights":
             s["step"] = zkv.PreparedAccumulate(
-                s["q"], s["lse"], s["k_codes"], s["comp_len"], s["Ck"], s["acc"], max_comp_len=c["T"],
+                s["q"], s["lse"], s["k_codes_pool"], s["comp_len"], s["Ck"], s["acc"], max_comp_len=c["T"],
                 block_table=s["table"])
         else:
             s["step"] = zkv.PreparedEvict(
@@ -464,7 +466,11 @@ def run(state):
     if op == "commit":
         s["lengths"].copy_(s["before"])      # the loop goes back to where the drafts were made
     if own:
-        _step(s)()
+        step = _step(s)
+        for x in ("k_codes", "v_codes"):     # pools that lie otherwise are laid out in every pass
+            if x in s and not s[x].is_contiguous():
+                s[x + "_pool"].copy_(s[x])
+        step()
     if op == "tree":
         return (s["out"], s["lse"]) if own else _tree(s)
     if op == "commit":
