@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace zkv {
 
@@ -264,19 +265,27 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s
   return __byte_perm(a, b, s);
 }
 
-// The codes of four tokens t .. t + 3 (t a multiple of 4; tokens from tend on read as code 0).
-template <int SP, int W>
+// The codes of four tokens t .. t + 3 (t a multiple of 4; tokens from tend on read as code 0).  FULL:
+// all four exist and rows are SP bytes.  Four rows lie together (capacities and pages are multiples
+// of 16 tokens).
+template <int SP, int W, bool FULL>
 __device__ __forceinline__ void load_four(const CodeRows& rows, uint32_t t, uint32_t tend, int S,
                                           uint32_t (&w)[4][W]) {
+  const uint8_t* p = nullptr;
+  if constexpr (FULL) {
+    if (!rows.table) {
+      p = rows.base + (uint64_t)t * SP;
+    } else {
+      p = rows.row(t, SP);
+    }
+  } else if (t < tend && (S == SP || S == 3)) {
+    p = rows.row(t, S);
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u)
 #pragma unroll
     for (int i = 0; i < W; ++i) w[u][i] = 0u;
-  if (t >= tend) return;
-  if (S == SP || S == 3) {
-    // four rows lie together (capacities and pages are multiples of 16 tokens), 4 S bytes
-    const uint8_t* p = rows.row(t, S);
-    if (!p) return;
+  if (p) {
     const unsigned int* p4 = reinterpret_cast<const unsigned int*>(p);
     if constexpr (SP == 1) {
       const uint32_t x = __ldg(p4);
@@ -287,7 +296,7 @@ __device__ __forceinline__ void load_four(const CodeRows& rows, uint32_t t, uint
       w[0][0] = x.x & 0xffffu; w[1][0] = x.x >> 16;
       w[2][0] = x.y & 0xffffu; w[3][0] = x.y >> 16;
     } else if constexpr (SP == 4) {
-      if (S == 4) {
+      if (FULL || S == 4) {
         const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
         w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
       } else {
@@ -303,7 +312,7 @@ __device__ __forceinline__ void load_four(const CodeRows& rows, uint32_t t, uint
       w[0][0] = x.x; w[0][W - 1] = x.y; w[1][0] = x.z; w[1][W - 1] = x.w;
       w[2][0] = y.x; w[2][W - 1] = y.y; w[3][0] = y.z; w[3][W - 1] = y.w;
     }
-  } else {
+  } else if (!FULL && S != SP && S != 3) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (t + u < tend) load_codes<SP>(rows, t + u, S, w[u]);
@@ -398,31 +407,42 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     bool chosen = false, dirty = false, folded = false, poison = false;
     float* slot = a.pw + (item + blockIdx.x) * (int64_t)(a.Sv * kCodebook * kTreeRG);
 
-    // score of one token for this lane's row
-    auto score = [&](const uint32_t (&w)[C::KW]) {
-      float s = 0.f;
+    // scores of two tokens for this lane's row, less the reference
+    auto score2 = [&](const uint32_t (&w0)[C::KW], const uint32_t (&w1)[C::KW], float neg_ref) {
+      float2 s = make_float2(neg_ref, neg_ref);
 #pragma unroll
-      for (int i = 0; i < SKP; ++i)
-        s += *reinterpret_cast<const float*>(sm + byte_perm(w[i >> 2 < C::KW ? i >> 2 : 0], kcol[i / 2], ksel[i]));
+      for (int i = 0; i < SKP; ++i) {
+        constexpr int W1 = C::KW - 1;
+        const uint32_t x0 = byte_perm(i < 4 ? w0[0] : w0[W1], kcol[i / 2], ksel[i]);
+        const uint32_t x1 = byte_perm(i < 4 ? w1[0] : w1[W1], kcol[i / 2], ksel[i]);
+        s = fadd2(s, make_float2(*reinterpret_cast<const float*>(sm + x0),
+                                 *reinterpret_cast<const float*>(sm + x1)));
+      }
       return s;
     };
-    // counters -> slot, times f (a reference that was raised); every thread keeps to its own row
+    const bool exact = a.Sk == SKP && a.Sv == SVP;
+    // counters -> slot, times f (a reference that was raised); lane (h, r) keeps to its own row r and
+    // to column h (stage or copy) of each codeword: whole 128-byte rows, no bank conflict
     auto fold = [&](float f) {
-      for (int x = tid; x < a.Sv * kCodebook * kTreeRG; x += C::THREADS) {
-        const int c = (x >> 3) & (kCodebook - 1), s = x >> 11;
-        uint32_t* p = reinterpret_cast<uint32_t*>(sm + C::VOFF + 256 * c + 32 * (s * C::VR)) + r;
-        float v = 0.f;
-        if (dirty) {
-          // the copies are separate counts of the same word
+#pragma unroll 4
+      for (int c = warp; c < kCodebook; c += C::NW) {
 #pragma unroll
-          for (int k = 0; k < C::VR; ++k) {
-            v += (float)p[8 * k];
-            p[8 * k] = 0u;
+        for (int q = 0; q < (SVP == 8 ? 2 : 1); ++q) {
+          const int s = (SVP >= 4 ? h : h / C::VR) + 4 * q;
+          uint32_t* p = reinterpret_cast<uint32_t*>(sm + C::VOFF + 256 * c + 128 * q) + lane;
+          float v = 0.f;
+          if (dirty) {
+            v = (float)*p;
+            *p = 0u;
+            if (SVP == 1) v += __shfl_xor_sync(0xffffffffu, v, 8);      // copies of one counter
+            if (SVP <= 2) v += __shfl_xor_sync(0xffffffffu, v, SVP == 1 ? 16 : 8);
+            v *= unit;
           }
-          v *= unit;
+          if (s < a.Sv && (C::VR == 1 || h % C::VR == 0)) {
+            float* o = slot + ((s * kCodebook + c) * kTreeRG + r);
+            *o = (folded ? v + *o : v) * f;
+          }
         }
-        if (folded) v += slot[x];
-        slot[x] = v * f;
       }
       folded = true;
       dirty = false;
@@ -458,10 +478,13 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       for (int k = 0; k < kTreeTK / 4; ++k) {
         const uint32_t t = t0 + ((k * C::NW + warp) * 4 + h) * 4;
         uint32_t w[4][C::KW];
-        load_four<SKP, C::KW>(kr, t, tend, a.Sk, w);
+        load_four<SKP, C::KW, false>(kr, t, tend, a.Sk, w);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (t + u < tend) mx = fmaxf(mx, score(w[u]));
+        for (int u = 0; u < 4; u += 2) {
+          const float2 x = score2(w[u], w[u + 1], 0.f);
+          if (t + u < tend) mx = fmaxf(mx, x.x);
+          if (t + u + 1 < tend) mx = fmaxf(mx, x.y);
+        }
       }
       publish(0.f, mx);
       float sum;
@@ -469,36 +492,51 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       ref = fabsf(mx) < 1e30f ? mx : 0.f;
     }
 
-    for (uint32_t tile = t0; tile < tend;) {
-      float p[kTreeTK];
-      uint32_t wv[kTreeTK][C::VW];
-      float sum = 0.f, mx = -INFINITY;
+    // p of this thread's tokens of a tile, their sum and largest score, their value codes
+    auto tile_scores = [&](auto full, uint32_t tile, float (&p)[kTreeTK],
+                           uint32_t (&wv)[kTreeTK / 4][4][C::VW], float& sum, float& mx) {
+      constexpr bool FULL = decltype(full)::value;
+      float2 sum2 = make_float2(0.f, 0.f);
+      mx = -INFINITY;
+      uint32_t wk[kTreeTK / 4][4][C::KW];
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k)
+        load_four<SKP, C::KW, FULL>(kr, tile + ((k * C::NW + warp) * 4 + h) * 4, tend, a.Sk, wk[k]);
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k)
+        load_four<SVP, C::VW, FULL>(vr, tile + ((k * C::NW + warp) * 4 + h) * 4, tend, a.Sv, wv[k]);
 #pragma unroll
       for (int k = 0; k < kTreeTK / 4; ++k) {
         const uint32_t t = tile + ((k * C::NW + warp) * 4 + h) * 4;
-        uint32_t wk[4][C::KW], w4[4][C::VW];
-        load_four<SKP, C::KW>(kr, t, tend, a.Sk, wk);
-        load_four<SVP, C::VW>(vr, t, tend, a.Sv, w4);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-          for (int i = 0; i < C::VW; ++i) wv[4 * k + u][i] = w4[u][i];
-          const float x = t + u < tend ? score(wk[u]) - ref : -INFINITY;
-          p[4 * k + u] = ex2_approx(x);
-          sum += p[4 * k + u];
-          mx = fmaxf(mx, x);
+        for (int u = 0; u < 4; u += 2) {
+          float2 x = score2(wk[k][u], wk[k][u + 1], -ref);
+          if constexpr (!FULL) {
+            if (t + u >= tend) x.x = -INFINITY;
+            if (t + u + 1 >= tend) x.y = -INFINITY;
+          }
+          mx = fmaxf(mx, fmaxf(x.x, x.y));
+          const float2 e = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+          sum2 = fadd2(sum2, e);
+          p[4 * k + u] = e.x;
+          p[4 * k + u + 1] = e.y;
         }
       }
+      sum = sum2.x + sum2.y;
+    };
+    for (uint32_t tile = t0; tile < tend;) {
+      float p[kTreeTK];
+      uint32_t wv[kTreeTK / 4][4][C::VW];
+      float sum, mx;
+      if (exact && tend - tile >= C::TILE) tile_scores(std::true_type{}, tile, p, wv, sum, mx);
+      else tile_scores(std::false_type{}, tile, p, wv, sum, mx);
       publish(sum, mx);
       collect(sum, mx);
       // every warp holds all eight rows and the same sums: the votes agree in the whole block
       const bool up = mx > 64.f && mx < 1e30f;
       if (__any_sync(0xffffffffu, up)) {
         // (all additions of the previous tile came before the barrier)
-        fold(up ? ex2_approx(-fminf(mx, 126.f)) : 1.f);
-        if (up && mx > 126.f) {   // 2^-mx is below float32: what the slot holds is nothing
-          for (int x = tid; x < a.Sv * kCodebook * kTreeRG; x += C::THREADS) slot[x] = 0.f;
-        }
+        fold(up ? ex2_ftz(-mx) : 1.f);
         if (up) ref += mx;
         chosen = false;
         __syncthreads();          // the counters are zero before anyone adds
@@ -523,13 +561,15 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       }
       used += sum * scale + (float)(C::TILE / 2);
       dirty = true;
+      const float mul = bad ? 0.f : scale;        // (inf and NaN times 0 convert to 0)
 #pragma unroll
       for (int k = 0; k < kTreeTK; ++k) {
-        const uint32_t u = bad ? 0u : __float2uint_rn(p[k] * scale);
+        const uint32_t u = __float2uint_rn(p[k] * mul);
 #pragma unroll
         for (int i = 0; i < SVP; ++i)
           atomicAdd(reinterpret_cast<uint32_t*>(
-                        sm + C::VOFF + byte_perm(wv[k][i >> 2 < C::VW ? i >> 2 : 0], vcol[i / 2], vsel[i])), u);
+                        sm + C::VOFF + byte_perm(wv[k / 4][k % 4][i < 4 ? 0 : C::VW - 1], vcol[i / 2], vsel[i])),
+                    u);
       }
       tile += C::TILE;
     }

@@ -212,6 +212,23 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// 2^x, approximate; results below the smallest normal float flush to zero (for
+// weights that are negligible there).
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two independent float32 additions in one instruction (each rounded as a scalar add).
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 __device__ __forceinline__ void set_error(int32_t* flag, int bits) {
   if (flag) atomicOr(flag, bits);
 }
