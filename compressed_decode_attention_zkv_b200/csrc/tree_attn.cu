@@ -234,100 +234,106 @@ __global__ void __launch_bounds__(kQtThreads) tree_prepare_kernel(TreeArgs a) {
 // ---------------------------------------------------------------------------------------------
 // 2. Scan
 // ---------------------------------------------------------------------------------------------
-// Lane = (token slot h = lane / 8, row r = lane % 8); a thread takes kTreeTK tokens of a tile for
-// one row.  Shared memory holds 256 rows (codewords) of 256 bytes: bytes [0, 128) the key table
-// entries [stage][copy][row] of the codeword, bytes [128, 256) its weight counters, so that the
-// address of either is one byte permutation [column | code] of the packed codes.  With 8 stages
-// on either side each kind has 256-byte rows of its own.  Slot h visits the stages in the order
-// s = i ^ h (fewer than four stages: copies), so the 32 lanes of every gather and every counter
-// addition lie in 32 distinct banks, whatever the codes are.
+// Lane = (token slot h = lane / 4, row pair r = lane % 4); a thread takes kTreeTK tokens of a tile
+// for rows 2 r and 2 r + 1.  Shared memory holds 256 rows (codewords) of 256 bytes: bytes [0, 128)
+// the key table entries [stage][copy][row] of the codeword, bytes [128, 256) its weight counters, so
+// that the address of either is one byte permutation [column | code] of the packed codes.  With 8
+// stages on either side each kind has 256-byte rows of its own.  Slot h visits the stages in the
+// order s = i ^ (h % 4) (fewer than four stages: copies) and slots 4 .. 7 add their odd row first, so
+// the lanes of every gather phase and of every counter addition lie in distinct banks, whatever the
+// codes are.
 //
 // Weights.  p = 2^(score - ref) with ref the row's maximum over the first tile.  The block sums p
 // per row over the tile before it adds any (one barrier), so a row's unit can be chosen: a power
 // of two with the first tile's sum at 2^27 .. 2^28 units.  Counters then take u = p / unit, rounded,
 // as exact integers in any order; when the sum of a row could pass 2^32 the counters are folded
 // into the slot (float32) and the unit chosen anew.  A rounding is half a unit, 2^-28 of a tile's
-// sum, per token.  A score 2^64 above ref (in p) folds and raises ref.
+// sum, per token.  A tile whose sum is above 2^64 is folded against its own maximum as the new ref.
 template <int SKP, int SVP>
 struct TreeScan {
   static constexpr bool WIDE = SKP == 8 || SVP == 8;
-  static constexpr int NW = WIDE ? 16 : 8;          // warps
+  static constexpr int NW = WIDE ? 16 : 12;         // warps
   static constexpr int THREADS = NW * 32;
-  static constexpr int TILE = NW * 4 * kTreeTK;     // tokens
+  static constexpr int TILE = NW * 8 * kTreeTK;     // tokens
   static constexpr int VOFF = WIDE ? 65536 : 128;   // weight counters of a codeword
   static constexpr int KR = SKP >= 4 ? 1 : 4 / SKP; // copies
   static constexpr int VR = SVP >= 4 ? 1 : 4 / SVP;
-  static constexpr int SMEM = (WIDE ? 131072 : 65536) + 4 * kTreeRG * NW * 4;
+  static constexpr int TABLES = WIDE ? 131072 : 65536;
+  static constexpr int SUMS = 2 * kTreeRG * NW * 4;
+  static constexpr int CODES = 32 * (kTreeTK / 4) * (SKP + SVP);   // bytes of a warp's part of a tile
+  static constexpr int SMEM = TABLES + SUMS + 2 * NW * CODES;
   static constexpr int KW = SKP <= 4 ? 1 : 2, VW = SVP <= 4 ? 1 : 2;   // code words per token
 };
 
+// Gathers and counter additions take the permuted bytes as a shared-memory address with the start of
+// the tables as an immediate offset: dynamic shared memory begins at kTreeSmemBase, behind the
+// reserved system area (the kernel checks it and reports ZKV_DEVERR_SMEM otherwise).  No memory
+// clobber: tables and counters are written and read on either side of a barrier.
+constexpr int kTreeSmemBase = 1024;
+__device__ __forceinline__ float2 tree_lds(uint32_t x) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2+%3];" : "=f"(v.x), "=f"(v.y) : "r"(x), "n"(kTreeSmemBase));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ void tree_red(uint32_t x, uint32_t u) {
+  asm volatile("red.shared.add.u32 [%0+%2], %1;" ::"r"(x), "r"(u), "n"(kTreeSmemBase + OFF));
+}
+
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
-  return __byte_perm(a, b, s);
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
+  return d;
 }
 
-// The codes of four tokens t .. t + 3 (t a multiple of 4; tokens from tend on read as code 0).  FULL:
-// all four exist and rows are SP bytes.  Four rows lie together (capacities and pages are multiples
-// of 16 tokens).
-template <int SP, int W, bool FULL>
-__device__ __forceinline__ void load_four(const CodeRows& rows, uint32_t t, uint32_t tend, int S,
-                                          uint32_t (&w)[4][W]) {
-  const uint8_t* p = nullptr;
-  if constexpr (FULL) {
-    if (!rows.table) {
-      p = rows.base + (uint64_t)t * SP;
+// The codes of four tokens from the warp's copy (p: the first one's S bytes; 4-byte aligned).  EXACT:
+// rows are SP bytes.
+template <int SP, int W, bool EXACT>
+__device__ __forceinline__ void read_four(const unsigned char* p, int S, uint32_t (&w)[4][W]) {
+  const uint32_t* p4 = reinterpret_cast<const uint32_t*>(p);
+  if constexpr (SP == 1) {
+    const uint32_t x = *p4;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u][0] = (x >> (8 * u)) & 255u;
+  } else if constexpr (SP == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0][0] = x.x & 0xffffu; w[1][0] = x.x >> 16;
+    w[2][0] = x.y & 0xffffu; w[3][0] = x.y >> 16;
+  } else if constexpr (SP == 4) {
+    if (EXACT || S == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
     } else {
-      p = rows.row(t, SP);
+      const uint32_t x = p4[0], y = p4[1], z = p4[2];
+      w[0][0] = x & 0xffffffu;
+      w[1][0] = __funnelshift_r(x, y, 24) & 0xffffffu;
+      w[2][0] = __funnelshift_r(y, z, 16) & 0xffffffu;
+      w[3][0] = z >> 8;
     }
-  } else if (t < tend && (S == SP || S == 3)) {
-    p = rows.row(t, S);
-  }
+  } else if (EXACT || S == 8) {
+    const uint4 x = reinterpret_cast<const uint4*>(p)[0], y = reinterpret_cast<const uint4*>(p)[1];
+    w[0][0] = x.x; w[0][W - 1] = x.y; w[1][0] = x.z; w[1][W - 1] = x.w;
+    w[2][0] = y.x; w[2][W - 1] = y.y; w[3][0] = y.z; w[3][W - 1] = y.w;
+  } else {
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
+      w[u][0] = w[u][W - 1] = 0u;
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[u][i] = 0u;
-  if (p) {
-    const unsigned int* p4 = reinterpret_cast<const unsigned int*>(p);
-    if constexpr (SP == 1) {
-      const uint32_t x = __ldg(p4);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u][0] = (x >> (8 * u)) & 255u;
-    } else if constexpr (SP == 2) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0][0] = x.x & 0xffffu; w[1][0] = x.x >> 16;
-      w[2][0] = x.y & 0xffffu; w[3][0] = x.y >> 16;
-    } else if constexpr (SP == 4) {
-      if (FULL || S == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0][0] = x.x; w[1][0] = x.y; w[2][0] = x.z; w[3][0] = x.w;
-      } else {
-        const uint32_t x = __ldg(p4), y = __ldg(p4 + 1), z = __ldg(p4 + 2);
-        w[0][0] = x & 0xffffffu;
-        w[1][0] = __funnelshift_r(x, y, 24) & 0xffffffu;
-        w[2][0] = __funnelshift_r(y, z, 16) & 0xffffffu;
-        w[3][0] = z >> 8;
-      }
-    } else {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint4 y = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-      w[0][0] = x.x; w[0][W - 1] = x.y; w[1][0] = x.z; w[1][W - 1] = x.w;
-      w[2][0] = y.x; w[2][W - 1] = y.y; w[3][0] = y.z; w[3][W - 1] = y.w;
+      for (int q = 0; q < 8; ++q)
+        if (q < S) w[u][q < 4 ? 0 : W - 1] |= (uint32_t)p[u * S + q] << (8 * (q & 3));
     }
-  } else if (!FULL && S != SP && S != 3) {
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (t + u < tend) load_codes<SP>(rows, t + u, S, w[u]);
   }
 }
 
-template <int SKP, int SVP>
-__global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP>::WIDE ? 1 : 3)
+template <int SKP, int SVP, bool PAGED>
+__global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP>::WIDE ? 1 : 2)
     tree_scan_kernel(TreeArgs a) {
   using C = TreeScan<SKP, SVP>;
   extern __shared__ __align__(16) unsigned char sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = lane & 7, h = lane >> 3;
-  float* sums = reinterpret_cast<float*>(sm + (C::WIDE ? 131072 : 65536));   // [2][8][NW]
-  float* maxs = sums + 2 * kTreeRG * C::NW;                                  // [2][8][NW]
+  const int r = lane & 3, h = lane >> 2;
+  float* sums = reinterpret_cast<float*>(sm + C::TABLES);                    // [2][8][NW]
+  unsigned char* codes = sm + C::TABLES + C::SUMS + warp * 2 * C::CODES;     // this warp's [2][K, V]
   pdl_trigger();
   // the weight counters start at zero and every fold leaves them at zero
   for (int f = tid; f < kCodebook * 8; f += C::THREADS) {
@@ -335,24 +341,35 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     *reinterpret_cast<uint4*>(z) = make_uint4(0, 0, 0, 0);
     if (SVP == 8) *reinterpret_cast<uint4*>(z + 128) = make_uint4(0, 0, 0, 0);
   }
-  // per-lane columns and selectors: step i of the stage loop
-  uint32_t kcol[(SKP + 1) / 2], vcol[(SVP + 1) / 2], ksel[SKP], vsel[SVP];
+  // per-lane columns of step i of the stage loop (byte i & 1; bytes 2 and 3 zero); v: first and second
+  // row of the pair.  A token's code word is first put into the lane's stage order (korder, vorder),
+  // so that the selectors of the address permutations are constants.
+  uint32_t kcol[(SKP + 1) / 2], vcol[2][(SVP + 1) / 2], korder = 0u, vorder = 0u;
+  const uint32_t h4 = (uint32_t)h & 3u, swap = (uint32_t)h >> 2;
 #pragma unroll
   for (int i = 0; i < (SKP + 1) / 2; ++i) kcol[i] = 0u;
 #pragma unroll
-  for (int i = 0; i < (SVP + 1) / 2; ++i) vcol[i] = 0u;
+  for (int i = 0; i < (SVP + 1) / 2; ++i) vcol[0][i] = vcol[1][i] = 0u;
 #pragma unroll
   for (int i = 0; i < SKP; ++i) {
-    const uint32_t s = (uint32_t)(i ^ h) & (SKP - 1), rep = SKP >= 4 ? 0u : (uint32_t)h / SKP;
-    kcol[i / 2] |= ((s * C::KR + rep) * 32u + r * 4u) << (8 * (i & 1));
-    ksel[i] = (4u + (i & 1)) | ((s & 3u) << 4) | (6u << 8) | (7u << 12);
+    const uint32_t s = ((uint32_t)i ^ h4) & (SKP - 1), rep = SKP >= 4 ? 0u : h4 / SKP;
+    kcol[i / 2] |= ((s * C::KR + rep) * 32u + r * 8u) << (8 * (i & 1));
+    if (i < 4) korder |= (s & 3u) << (4 * i);
   }
 #pragma unroll
   for (int i = 0; i < SVP; ++i) {
-    const uint32_t s = (uint32_t)(i ^ h) & (SVP - 1), rep = SVP >= 4 ? 0u : (uint32_t)h / SVP;
-    vcol[i / 2] |= ((s * C::VR + rep) * 32u + r * 4u) << (8 * (i & 1));
-    vsel[i] = (4u + (i & 1)) | ((s & 3u) << 4) | (6u << 8) | (7u << 12);
+    const uint32_t s = ((uint32_t)i ^ h4) & (SVP - 1), rep = SVP >= 4 ? 0u : h4 / SVP;
+#pragma unroll
+    for (uint32_t v = 0; v < 2; ++v)
+      vcol[v][i / 2] |= ((s * C::VR + rep) * 32u + r * 8u + (v ^ swap) * 4u) << (8 * (i & 1));
+    if (i < 4) vorder |= (s & 3u) << (4 * i);
   }
+  // (kept in registers: not worth computing again in every tile)
+  asm volatile("" : "+r"(korder), "+r"(vorder));
+#pragma unroll
+  for (int i = 0; i < (SKP + 1) / 2; ++i) asm volatile("" : "+r"(kcol[i]));
+#pragma unroll
+  for (int i = 0; i < (SVP + 1) / 2; ++i) asm volatile("" : "+r"(vcol[0][i]), "+r"(vcol[1][i]));
   pdl_wait();
   const int64_t per = a.pre[a.B + 1];
   const int64_t items_per_b = (int64_t)a.Hkv * a.NRG;
@@ -360,6 +377,10 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
   int64_t lo = blockIdx.x * per;
   const int64_t hi = lo + per < total ? lo + per : total;
   if (lo >= hi) return;
+  if ((uint32_t)__cvta_generic_to_shared(sm) != kTreeSmemBase) {   // (the slots stay unwritten)
+    if (tid == 0) set_error(a.err, ZKV_DEVERR_SMEM);
+    return;
+  }
   // the sequence of the first unit: the last b with pre[b] * items_per_b <= lo
   int b = 0;
   {
@@ -403,43 +424,54 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       __syncthreads();
     }
 
-    float ref = 0.f, scale = 0.f, unit = 0.f, used = 0.f;
-    bool chosen = false, dirty = false, folded = false, poison = false;
+    // state of this thread's two rows (the same in every thread that has them)
+    float ref[2];                  // (NaN from the first sum on that is not finite: the row is lost)
+    float scale[2] = {1.f, 1.f}, used[2] = {0.f, 0.f};     // 1 / unit; the sum since the last fold
+    bool chosen = false, dirty = false, folded = false;
     float* slot = a.pw + (item + blockIdx.x) * (int64_t)(a.Sv * kCodebook * kTreeRG);
+    const bool exact = a.Sk == SKP && a.Sv == SVP;
+    auto first_of = [&](uint32_t tile, int k) { return tile + ((k * C::NW + warp) * 8 + h) * 4; };
 
-    // scores of two tokens for this lane's row, less the reference
-    auto score2 = [&](const uint32_t (&w0)[C::KW], const uint32_t (&w1)[C::KW], float neg_ref) {
-      float2 s = make_float2(neg_ref, neg_ref);
+    // scores of a token for this lane's rows, less the references
+    auto score = [&](const uint32_t (&w)[C::KW], float2 neg_ref) {
+      float2 s = neg_ref;
+      uint32_t x[C::KW];
 #pragma unroll
-      for (int i = 0; i < SKP; ++i) {
-        constexpr int W1 = C::KW - 1;
-        const uint32_t x0 = byte_perm(i < 4 ? w0[0] : w0[W1], kcol[i / 2], ksel[i]);
-        const uint32_t x1 = byte_perm(i < 4 ? w1[0] : w1[W1], kcol[i / 2], ksel[i]);
-        s = fadd2(s, make_float2(*reinterpret_cast<const float*>(sm + x0),
-                                 *reinterpret_cast<const float*>(sm + x1)));
-      }
+      for (int i = 0; i < C::KW; ++i) x[i] = byte_perm(w[i], 0u, korder);
+#pragma unroll
+      for (int i = 0; i < SKP; ++i)
+        s = fadd2(s, tree_lds(byte_perm(x[i < 4 ? 0 : C::KW - 1], kcol[i / 2],
+                                        (4u + (i & 1)) | ((i & 3u) << 4) | 0x7600u)));
       return s;
     };
-    const bool exact = a.Sk == SKP && a.Sv == SVP;
-    // counters -> slot, times f (a reference that was raised); lane (h, r) keeps to its own row r and
-    // to column h (stage or copy) of each codeword: whole 128-byte rows, no bank conflict
-    auto fold = [&](float f) {
+    // the value of row x = lane % 8 from the threads that have it
+    auto of_row = [&](const float (&v)[2]) {
+      const float v0 = __shfl_sync(0xffffffffu, v[0], (lane & 7) >> 1);
+      const float v1 = __shfl_sync(0xffffffffu, v[1], (lane & 7) >> 1);
+      return lane & 1 ? v1 : v0;
+    };
+    // counters -> slot, times f (a reference that was raised); lane = word of the codeword's 128-byte
+    // row: stage (or copy) lane / 8, row lane % 8
+    auto fold = [&](const float (&factor)[2]) {
+      // unit = 1 / scale, a power of two
+      const float f = of_row(factor), un = __uint_as_float(0x7F000000u - __float_as_uint(of_row(scale)));
+      const int col = lane >> 3;
 #pragma unroll 4
       for (int c = warp; c < kCodebook; c += C::NW) {
 #pragma unroll
         for (int q = 0; q < (SVP == 8 ? 2 : 1); ++q) {
-          const int s = (SVP >= 4 ? h : h / C::VR) + 4 * q;
+          const int s = (SVP >= 4 ? col : col / C::VR) + 4 * q;
           uint32_t* p = reinterpret_cast<uint32_t*>(sm + C::VOFF + 256 * c + 128 * q) + lane;
           float v = 0.f;
           if (dirty) {
             v = (float)*p;
             *p = 0u;
-            if (SVP == 1) v += __shfl_xor_sync(0xffffffffu, v, 8);      // copies of one counter
-            if (SVP <= 2) v += __shfl_xor_sync(0xffffffffu, v, SVP == 1 ? 16 : 8);
-            v *= unit;
+            if (SVP <= 2) v += __shfl_xor_sync(0xffffffffu, v, 8);      // copies of one counter
+            if (SVP == 1) v += __shfl_xor_sync(0xffffffffu, v, 16);
+            v *= un;
           }
-          if (s < a.Sv && (C::VR == 1 || h % C::VR == 0)) {
-            float* o = slot + ((s * kCodebook + c) * kTreeRG + r);
+          if (s < a.Sv && (C::VR == 1 || col % C::VR == 0)) {
+            float* o = slot + ((s * kCodebook + c) * kTreeRG + (lane & 7));
             *o = (folded ? v + *o : v) * f;
           }
         }
@@ -447,136 +479,206 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       folded = true;
       dirty = false;
     };
-
-    // the reference: the row's maximum over the first tile
-    auto publish = [&](float sum, float mx) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      if (lane < 8) {
-        sums[(buf * kTreeRG + r) * C::NW + warp] = sum;
-        maxs[(buf * kTreeRG + r) * C::NW + warp] = mx;
-      }
+    // one value per row and thread -> one per row and warp (op) -> x of the block's rows; a barrier
+    auto exchange = [&](float2 v, auto op, float (&x)[2]) {
+      float t = (h & 1) ? v.x : v.y, k = (h & 1) ? v.y : v.x;      // lane keeps row 2 r + h % 2
+      k = op(k, __shfl_xor_sync(0xffffffffu, t, 4));
+      k = op(k, __shfl_xor_sync(0xffffffffu, k, 8));
+      k = op(k, __shfl_xor_sync(0xffffffffu, k, 16));
+      if (h < 2) sums[(buf * kTreeRG + 2 * r + h) * C::NW + warp] = k;
       __syncthreads();
-    };
-    auto collect = [&](float& sum, float& mx) {
-      sum = 0.f;
-      mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < C::NW; w += 4) {
-        const float4 s4 = *reinterpret_cast<const float4*>(sums + (buf * kTreeRG + r) * C::NW + w);
-        const float4 m4 = *reinterpret_cast<const float4*>(maxs + (buf * kTreeRG + r) * C::NW + w);
-        sum += (s4.x + s4.y) + (s4.z + s4.w);
-        mx = fmaxf(mx, fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)));
-      }
-      buf ^= 1;
-    };
-    {
-      float mx = -INFINITY;
+      for (int j = 0; j < 2; ++j) {
+        const float* p = sums + (buf * kTreeRG + 2 * r + j) * C::NW;
 #pragma unroll
-      for (int k = 0; k < kTreeTK / 4; ++k) {
-        const uint32_t t = t0 + ((k * C::NW + warp) * 4 + h) * 4;
-        uint32_t w[4][C::KW];
-        load_four<SKP, C::KW, false>(kr, t, tend, a.Sk, w);
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          const float2 x = score2(w[u], w[u + 1], 0.f);
-          if (t + u < tend) mx = fmaxf(mx, x.x);
-          if (t + u + 1 < tend) mx = fmaxf(mx, x.y);
+        for (int w = 0; w < C::NW; w += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(p + w);
+          const float y = op(op(s4.x, s4.y), op(s4.z, s4.w));
+          x[j] = w ? op(x[j], y) : y;
         }
       }
-      publish(0.f, mx);
-      float sum;
-      collect(sum, mx);
-      ref = fabsf(mx) < 1e30f ? mx : 0.f;
-    }
+      buf ^= 1;      // the next exchange's barrier lies between two uses of a buffer
+    };
+    auto add = [](float x, float y) { return x + y; };
+    auto larger = [](float x, float y) { return fmaxf(x, y); };
 
-    // p of this thread's tokens of a tile, their sum and largest score, their value codes
-    auto tile_scores = [&](auto full, uint32_t tile, float (&p)[kTreeTK],
-                           uint32_t (&wv)[kTreeTK / 4][4][C::VW], float& sum, float& mx) {
-      constexpr bool FULL = decltype(full)::value;
-      float2 sum2 = make_float2(0.f, 0.f);
-      mx = -INFINITY;
-      uint32_t wk[kTreeTK / 4][4][C::KW];
-#pragma unroll
-      for (int k = 0; k < kTreeTK / 4; ++k)
-        load_four<SKP, C::KW, FULL>(kr, tile + ((k * C::NW + warp) * 4 + h) * 4, tend, a.Sk, wk[k]);
-#pragma unroll
-      for (int k = 0; k < kTreeTK / 4; ++k)
-        load_four<SVP, C::VW, FULL>(vr, tile + ((k * C::NW + warp) * 4 + h) * 4, tend, a.Sv, wv[k]);
-#pragma unroll
-      for (int k = 0; k < kTreeTK / 4; ++k) {
-        const uint32_t t = tile + ((k * C::NW + warp) * 4 + h) * 4;
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          float2 x = score2(wk[k][u], wk[k][u + 1], -ref);
-          if constexpr (!FULL) {
-            if (t + u >= tend) x.x = -INFINITY;
-            if (t + u + 1 >= tend) x.y = -INFINITY;
+    // This warp's codes of a tile, copied ahead in 16-byte pieces: 32 tokens in a row for each k, a
+    // multiple of 16 bytes whatever S is (capacities and pages are multiples of 16 tokens, so a piece
+    // neither crosses a page nor leaves the array).  Pieces behind the last token are not copied.
+    auto fetch_kind = [&](auto sc, const CodeRows& rows, int Srt, uint32_t tile, unsigned char* dst) {
+      const int S = decltype(sc)::value ? decltype(sc)::value : Srt;
+      for (int x = lane; x < 2 * S * (kTreeTK / 4); x += 32) {
+        const int k = x / (2 * S), piece = x - k * 2 * S;
+        const uint32_t first = tile + (k * C::NW + warp) * 32;
+        const uint64_t byte = (uint64_t)first * S + 16 * piece;
+        if (byte >= (uint64_t)tend * S) continue;
+        const uint8_t* src = rows.base + byte;
+        if constexpr (PAGED) {
+          const uint32_t t = first + 16 * piece / S, t0p = t >> rows.pshift << rows.pshift;
+          src = rows.row(t0p, S);
+          if (!src) {
+            *reinterpret_cast<uint4*>(dst + 16 * x) = make_uint4(0, 0, 0, 0);
+            continue;
           }
-          mx = fmaxf(mx, fmaxf(x.x, x.y));
-          const float2 e = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
-          sum2 = fadd2(sum2, e);
-          p[4 * k + u] = e.x;
-          p[4 * k + u + 1] = e.y;
+          src += byte - (uint64_t)t0p * S;
+        }
+        cp_async16(dst + 16 * x, src);
+      }
+    };
+    auto fetch = [&](uint32_t tile, int q) {
+      unsigned char *dk = codes + q * C::CODES, *dv = dk + 32 * (kTreeTK / 4) * SKP;
+      if (tile < tend) {
+        if (exact) {
+          fetch_kind(std::integral_constant<int, SKP>{}, kr, 0, tile, dk);
+          fetch_kind(std::integral_constant<int, SVP>{}, vr, 0, tile, dv);
+        } else {
+          fetch_kind(std::integral_constant<int, 0>{}, kr, a.Sk, tile, dk);
+          fetch_kind(std::integral_constant<int, 0>{}, vr, a.Sv, tile, dv);
         }
       }
-      sum = sum2.x + sum2.y;
+      cp_async_commit();
     };
-    for (uint32_t tile = t0; tile < tend;) {
-      float p[kTreeTK];
-      uint32_t wv[kTreeTK / 4][4][C::VW];
-      float sum, mx;
-      if (exact && tend - tile >= C::TILE) tile_scores(std::true_type{}, tile, p, wv, sum, mx);
-      else tile_scores(std::false_type{}, tile, p, wv, sum, mx);
-      publish(sum, mx);
-      collect(sum, mx);
-      // every warp holds all eight rows and the same sums: the votes agree in the whole block
-      const bool up = mx > 64.f && mx < 1e30f;
-      if (__any_sync(0xffffffffu, up)) {
-        // (all additions of the previous tile came before the barrier)
-        fold(up ? ex2_ftz(-mx) : 1.f);
-        if (up) ref += mx;
-        chosen = false;
-        __syncthreads();          // the counters are zero before anyone adds
-        continue;                 // the same tile against the new reference
+    auto key_codes = [&](auto ex, int q, int k, uint32_t (&w)[4][C::KW]) {
+      const int S = decltype(ex)::value ? SKP : a.Sk;
+      read_four<SKP, C::KW, decltype(ex)::value>(codes + q * C::CODES + (32 * k + 4 * h) * S, S, w);
+    };
+    auto value_codes = [&](auto ex, int q, int k, uint32_t (&w)[4][C::VW]) {
+      const int S = decltype(ex)::value ? SVP : a.Sv;
+      read_four<SVP, C::VW, decltype(ex)::value>(
+          codes + q * C::CODES + 32 * (kTreeTK / 4) * SKP + (32 * k + 4 * h) * S, S, w);
+    };
+    // the rows' largest scores of the tile
+    auto tile_max = [&](uint32_t tile, int q, float (&x)[2]) {
+      float2 mx = make_float2(-INFINITY, -INFINITY);
+#pragma unroll 1
+      for (int k = 0; k < kTreeTK / 4; ++k) {
+        uint32_t w[4][C::KW];
+        key_codes(std::false_type{}, q, k, w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 s = score(w[u], make_float2(0.f, 0.f));
+          if (first_of(tile, k) + u < tend) mx = make_float2(fmaxf(mx.x, s.x), fmaxf(mx.y, s.y));
+        }
       }
-      const bool bad = !(sum < 3e38f);
-      poison = poison || bad;
-      const float need = sum * scale + (float)(C::TILE / 2);
-      const bool full = !chosen || used + need > 4.0e9f;
-      if (__any_sync(0xffffffffu, full && !bad)) {
+      exchange(mx, larger, x);
+    };
+    // p of this thread's tokens of a tile and their sums
+    auto tile_scores = [&](auto full, uint32_t tile, int q, float2 (&p)[kTreeTK]) {
+      constexpr bool FULL = decltype(full)::value;
+      float2 sum = make_float2(0.f, 0.f);
+      const float2 neg = make_float2(-ref[0], -ref[1]);
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k) {
+        uint32_t w[4][C::KW];
+        key_codes(full, q, k, w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float2 x = score(w[u], neg);
+          if constexpr (!FULL)
+            if (first_of(tile, k) + u >= tend) x = make_float2(-INFINITY, -INFINITY);
+          p[4 * k + u] = make_float2(ex2_ftz(x.x), ex2_ftz(x.y));
+          sum = fadd2(sum, p[4 * k + u]);
+        }
+      }
+      return sum;
+    };
+    auto tile_add = [&](auto ex, int q, const float2 (&p)[kTreeTK], const float (&mul)[2]) {
+#pragma unroll
+      for (int k = 0; k < kTreeTK / 4; ++k) {
+        uint32_t w[4][C::VW];
+        value_codes(ex, q, k, w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t u0 = __float2uint_rn(p[4 * k + u].x * mul[0]);
+          const uint32_t u1 = __float2uint_rn(p[4 * k + u].y * mul[1]);
+          const uint32_t ua = swap ? u1 : u0, ub = swap ? u0 : u1;
+          uint32_t x[C::VW];
+#pragma unroll
+          for (int i = 0; i < C::VW; ++i) x[i] = byte_perm(w[u][i], 0u, vorder);
+#pragma unroll
+          for (int i = 0; i < SVP; ++i) {
+            const uint32_t y = x[i < 4 ? 0 : C::VW - 1], sel = (4u + (i & 1)) | ((i & 3u) << 4) | 0x7600u;
+            tree_red<C::VOFF>(byte_perm(y, vcol[0][i / 2], sel), ua);
+            tree_red<C::VOFF>(byte_perm(y, vcol[1][i / 2], sel), ub);
+          }
+        }
+      }
+    };
+
+    fetch(t0, 0);
+    cp_async_wait_all();
+    __syncwarp();
+    tile_max(t0, 0, ref);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (!(fabsf(ref[j]) < 1e30f)) ref[j] = 0.f;
+    int q = 0;
+    for (uint32_t tile = t0; tile < tend; tile += C::TILE, q ^= 1) {
+      fetch(tile + C::TILE, q ^ 1);      // (this warp has read that buffer's tile)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
+      float2 p[kTreeTK];
+      float sum[2];
+      for (int again = 0; again < 2; ++again) {
+        const float2 s2 = exact && tend - tile >= C::TILE ? tile_scores(std::true_type{}, tile, q, p)
+                                                          : tile_scores(std::false_type{}, tile, q, p);
+        exchange(s2, add, sum);
+        // every warp holds all eight rows and the same sums: the votes agree in the whole block
+        const bool up = (sum[0] > 0x1p64f || sum[1] > 0x1p64f) && !again;
+        if (!__any_sync(0xffffffffu, up)) break;
+        float mx[2], f[2];
+        tile_max(tile, q, mx);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool raise = sum[j] > 0x1p64f && mx[j] < 1e30f;
+          f[j] = raise ? ex2_ftz(ref[j] - mx[j]) : 1.f;
+          if (raise) ref[j] = mx[j];
+        }
+        fold(f);                   // (all additions of the previous tile came before the barrier)
+        chosen = false;
+        __syncthreads();           // the counters are zero before anyone adds
+      }
+      bool bad[2], full = false;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        bad[j] = !(sum[j] < 3e38f);
+        if (bad[j]) ref[j] = NAN;
+        full = full || (!bad[j] && used[j] + sum[j] * scale[j] + (float)(C::TILE / 2) > 4.0e9f);
+      }
+      if (__any_sync(0xffffffffu, full || !chosen)) {
         if (dirty) {
-          fold(1.f);
+          const float one[2] = {1.f, 1.f};
+          fold(one);
           __syncthreads();
         }
-        // sum = m 2^e, m in [1/2, 1): unit = 2^(e - 28)
-        int e = (int)((__float_as_uint(sum) >> 23) & 255u) - 126;
-        e = e < -90 ? -90 : e;
-        scale = __uint_as_float((uint32_t)(28 - e + 127) << 23);
-        unit = __uint_as_float((uint32_t)(e - 28 + 127) << 23);
-        used = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // sum = m 2^e, m in [1/2, 1): the unit is 2^(e - 28)
+          int e = (int)((__float_as_uint(sum[j]) >> 23) & 255u) - 126;
+          e = e < -90 ? -90 : e > 100 ? 100 : e;
+          scale[j] = __uint_as_float((uint32_t)(28 - e + 127) << 23);
+          used[j] = 0.f;
+        }
         chosen = true;
       }
-      used += sum * scale + (float)(C::TILE / 2);
-      dirty = true;
-      const float mul = bad ? 0.f : scale;        // (inf and NaN times 0 convert to 0)
+      float mul[2];
 #pragma unroll
-      for (int k = 0; k < kTreeTK; ++k) {
-        const uint32_t u = __float2uint_rn(p[k] * mul);
-#pragma unroll
-        for (int i = 0; i < SVP; ++i)
-          atomicAdd(reinterpret_cast<uint32_t*>(
-                        sm + C::VOFF + byte_perm(wv[k / 4][k % 4][i < 4 ? 0 : C::VW - 1], vcol[i / 2], vsel[i])),
-                    u);
+      for (int j = 0; j < 2; ++j) {
+        mul[j] = bad[j] ? 0.f : scale[j];        // (inf and NaN times 0 convert to 0)
+        used[j] += sum[j] * mul[j] + (float)(C::TILE / 2);
       }
-      tile += C::TILE;
+      dirty = true;
+      if (exact) tile_add(std::true_type{}, q, p, mul);
+      else tile_add(std::false_type{}, q, p, mul);
+      __syncwarp();        // every lane has read the codes
     }
     __syncthreads();
-    fold(1.f);
-    if (warp == 0 && lane < 8)
-      a.pm[(item + blockIdx.x) * kTreeRG + r] = poison ? NAN : ref;
+    const float one[2] = {1.f, 1.f};
+    fold(one);
+    if (warp == 0 && h == 0)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        a.pm[(item + blockIdx.x) * kTreeRG + 2 * r + j] = ref[j];
     lo += cnt;
   }
 }
@@ -770,7 +872,7 @@ static TreePlan tree_plan(const zkv_tree_params* p) {
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     sms = 148;
   const int64_t units = t.items * ((p->max_comp_len + kTreeUnit - 1) / kTreeUnit);
-  const int64_t ctas = (int64_t)sms * (t.SKP == 8 || t.SVP == 8 ? 1 : 3);
+  const int64_t ctas = (int64_t)sms * (t.SKP == 8 || t.SVP == 8 ? 1 : 2);
   t.grid = (int)std::max<int64_t>(1, std::min(ctas, (units + kTreeMinUnits - 1) / kTreeMinUnits));
   t.slots = t.items + t.grid;
   size_t o = 0;
@@ -826,9 +928,10 @@ static int validate_tree(const zkv_tree_params* p) {
 template <int SKP, int SVP>
 static cudaError_t launch_tree_scan(const TreeArgs& a, cudaStream_t st) {
   using C = TreeScan<SKP, SVP>;
-  const cudaError_t e = ensure_smem_limit(tree_scan_kernel<SKP, SVP>, C::SMEM);
+  void (*kernel)(TreeArgs) = a.table ? tree_scan_kernel<SKP, SVP, true> : tree_scan_kernel<SKP, SVP, false>;
+  const cudaError_t e = ensure_smem_limit(kernel, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_scan_kernel<SKP, SVP>, dim3(a.grid), dim3(C::THREADS), C::SMEM, st, a);
+  return launch_pdl(kernel, dim3(a.grid), dim3(C::THREADS), C::SMEM, st, a);
 }
 
 template <int SKP>
