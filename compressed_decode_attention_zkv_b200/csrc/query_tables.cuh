@@ -7,11 +7,14 @@
 // (float32, rho = group * RG + r), so that a token's base-2 score is sum_s T[zk_s][s][r].
 // Stages s >= Sk up to the padded count SKP, rows rho >= N G and rows of absent queries are 0.
 //
-// The work is a float32 product [256 codewords] x [d] x [rows]; block = 64 codewords of one stage
-// x 64 rows of one kv head (rows of several sequences side by side: they share the codewords).
+// The work is a product [rows] x [d] x [256 codewords] per kv head and stage with float32 accuracy
+// (mma_split.cuh).  Block = 64 rows of one kv head (rows of several sequences side by side: they
+// share the codewords) x one stage; it rotates its rows once and takes the codewords in chunks of
+// 64, the next chunk's loads in flight during a chunk's products.  With few blocks the chunks of a
+// stage are shared out over 2 or 4 blocks.
 #pragma once
 
-#include "zkv_internal.cuh"
+#include "mma_split.cuh"
 
 namespace zkv {
 
@@ -31,9 +34,12 @@ struct QueryTables {
   float* lut;     // [B * Hkv][RP / RG][256][SKP][RG]
 
   __host__ __device__ int row_blocks() const { return (int)(((int64_t)B * RP + kQtRows - 1) / kQtRows); }
-  __host__ __device__ int64_t blocks() const {
-    return (int64_t)(kCodebook / kQtCodes) * SKP * row_blocks() * Hkv;
+  // blocks that share the chunks of a stage: at least one block per SM where the chunks allow it
+  __host__ __device__ int shares() const {
+    const int64_t n = (int64_t)SKP * row_blocks() * Hkv;
+    return n >= 148 ? 1 : n >= 74 ? 2 : 4;
   }
+  __host__ __device__ int64_t blocks() const { return (int64_t)shares() * SKP * row_blocks() * Hkv; }
 };
 
 inline size_t query_tables_bytes(int64_t pairs, int RP, int SKP) {
@@ -48,98 +54,156 @@ __device__ __forceinline__ int present_queries(const int32_t* n, int b, int N) {
 
 template <int D>
 struct QtSmem {
-  float c[kQtCodes * D];          // codewords, 16-byte pieces swizzled by codeword
-  float qT[D][kQtRows + 4];       // rotated queries, transposed
+  __half q[2][kQtRows * D];       // rotated queries: high and low plane
+  __half c[2][kQtCodes * D];      // codewords
+  float qs[kQtRows];              // their scales (softmax scale included)
+  float cs[kQtCodes];
 };
 
 template <int D>
 __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t blk, QtSmem<D>& sm) {
   constexpr int E = D / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int shares = a.shares(), chunks = kCodebook / kQtCodes / shares;
   int64_t rest = blk;
-  const int c0 = (int)(rest % (kCodebook / kQtCodes)) * kQtCodes;
-  rest /= kCodebook / kQtCodes;
+  const int c0 = (int)(rest % shares) * chunks * kQtCodes;
+  rest /= shares;
   const int s = (int)(rest % a.SKP);
   rest /= a.SKP;
   const int row0 = (int)(rest % a.row_blocks()) * kQtRows;
   const int kvh = (int)(rest / a.row_blocks());
   const bool real = s < a.Sk;
-  if (real) {
-    const float* C = a.Ck + (((size_t)kvh * a.Sk + s) * kCodebook + c0) * D;
-    for (int f = tid; f < kQtCodes * D / 4; f += kQtThreads) {
-      const int c = f / (D / 4), p = f % (D / 4);
-      cp_async16(sm.c + c * D + 4 * (p ^ (c & 7)), C + (size_t)c * D + 4 * p);
+  // warp w loads codewords 8 w .. 8 w + 7 of a chunk, lane = E dimensions in a row
+  float cw[8][E];
+  auto load = [&](int chunk) {
+    const float* C = a.Ck + (((size_t)kvh * a.Sk + s) * kCodebook + c0 + chunk * kQtCodes + 8 * warp) * D;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* x = C + k * D + lane * E;
+      if constexpr (E == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(x));
+        cw[k][0] = v.x; cw[k][1] = v.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(x + e));
+          cw[k][e] = v.x; cw[k][e + 1] = v.y; cw[k][e + 2] = v.z; cw[k][e + 3] = v.w;
+        }
+      }
     }
-    cp_async_commit();
-    // the block's rows, rotated (float32 transform): warp w takes rows w, w + 8, ...
+  };
+  if (real) {
+    load(0);
+    // the block's rows, rotated (float32 transform): warp w takes rows 8 w .. 8 w + 7
+    float v[8][E];
+#pragma unroll
     for (int k = 0; k < kQtRows / 8; ++k) {
-      const int j = row0 + warp + 8 * k;
-      const int b = j / a.RP, rho = j % a.RP;
-      float v[E];
+      const int j = row0 + 8 * warp + k, b = j / a.RP, rho = j % a.RP;
+      const bool there = b < a.B && rho < a.R && rho / a.G < present_queries(a.n_query, b, a.N);
+      const __half* qr = a.q + b * a.q_sb + (rho / a.G) * a.q_sn +
+                         ((int64_t)kvh * a.G + rho % a.G) * a.q_sh + lane;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
-      if (b < a.B && rho < a.R && rho / a.G < present_queries(a.n_query, b, a.N)) {
-        const __half* qr = a.q + b * a.q_sb + (rho / a.G) * a.q_sn +
-                           ((int64_t)kvh * a.G + rho % a.G) * a.q_sh + lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = __half2float(qr[e * 32]);
-        if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
-          const float* l = a.k_smooth + (int64_t)kvh * D + lane;
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] *= l[e * 32];
-        }
-        fwht_warp_f32<D>(v, lane);
-        const float rs = (float)a.rot;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= rs;
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) sm.qT[e * 32 + lane][warp + 8 * k] = v[e];
+      for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
     }
-    cp_async_wait_all();
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kQtRows / 8; ++k) {
+      const int r = 8 * warp + k;
+      if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
+        const float* l = a.k_smooth + (int64_t)kvh * D + lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] *= l[e * 32];
+      }
+      fwht_warp_f32<D>(v[k], lane);
+      float big = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[k][e]));
+      const int ex = split_exponent(warp_max_f32(big));
+      const float down = exp2_int(-ex);
+      if (lane == 0) sm.qs[r] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int at = tile_at<D>(r, e * 32 + lane);
+        split(v[k][e] * down, sm.q[0][at], sm.q[1][at]);
+      }
+    }
   }
-  // thread = 4 codewords (cc + 16 u) x 4 rows (4 rq ..)
-  const int cc = tid & 15, rq = tid >> 4;
-  float acc[4][4];
+  const int wr = warp & 3, wc = warp >> 2;      // rows 16 wr .., codewords 32 wc .. of the chunk
+  const int g = lane >> 2, t4 = lane & 3;
+  // this thread's two rows in the tables (null: behind the last)
+  float* out[2];
 #pragma unroll
-  for (int u = 0; u < 4; ++u)
+  for (int q = 0; q < 2; ++q) {
+    const int j = row0 + 16 * wr + g + 8 * q, b = j / a.RP, rho = j % a.RP;
+    out[q] = b < a.B ? a.lut + (((int64_t)b * a.Hkv + kvh) * (a.RP / a.RG) + rho / a.RG) *
+                                   ((int64_t)kCodebook * a.SKP * a.RG) + rho % a.RG
+                     : nullptr;
+  }
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    float acc[4][4], cross[4][4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[u][v] = 0.f;
-  if (real) {
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = cross[n][i] = 0.f;
+    if (real) {
+      __syncthreads();              // the previous chunk has been read
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = 8 * warp + k;
+        float big = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(cw[k][e]));
+        const int ex = split_exponent(warp_max_f32(big));
+        const float down = exp2_int(-ex);
+        if (lane == 0) sm.cs[c] = exp2_int(ex);
+        alignas(16) __half hi[E], lo[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
+        const int at = tile_at<D>(c, lane * E);
+        if constexpr (E == 2) {
+          *reinterpret_cast<uint32_t*>(sm.c[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
+          *reinterpret_cast<uint32_t*>(sm.c[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
+        } else if constexpr (E == 4) {
+          *reinterpret_cast<uint2*>(sm.c[0] + at) = make_uint2(reinterpret_cast<const uint32_t*>(hi)[0], reinterpret_cast<const uint32_t*>(hi)[1]);
+          *reinterpret_cast<uint2*>(sm.c[1] + at) = make_uint2(reinterpret_cast<const uint32_t*>(lo)[0], reinterpret_cast<const uint32_t*>(lo)[1]);
+        } else {
+          const uint32_t *h4 = reinterpret_cast<const uint32_t*>(hi), *l4 = reinterpret_cast<const uint32_t*>(lo);
+          *reinterpret_cast<uint4*>(sm.c[0] + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+          *reinterpret_cast<uint4*>(sm.c[1] + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        }
+      }
+      __syncthreads();
+      if (chunk + 1 < chunks) load(chunk + 1);
 #pragma unroll 2
-    for (int p = 0; p < D / 4; ++p) {
-      float4 cv[4];
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t ah[4], al[4];
+        frag_a<D>(ah, sm.q[0], 16 * wr, ks, lane);
+        frag_a<D>(al, sm.q[1], 16 * wr, ks, lane);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        cv[u] = *reinterpret_cast<const float4*>(sm.c + (cc + 16 * u) * D + 4 * (p ^ (cc & 7)));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 q4 = *reinterpret_cast<const float4*>(&sm.qT[4 * p + e][4 * rq]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float x = e == 0 ? cv[u].x : e == 1 ? cv[u].y : e == 2 ? cv[u].z : cv[u].w;
-          acc[u][0] = fmaf(q4.x, x, acc[u][0]);
-          acc[u][1] = fmaf(q4.y, x, acc[u][1]);
-          acc[u][2] = fmaf(q4.z, x, acc[u][2]);
-          acc[u][3] = fmaf(q4.w, x, acc[u][3]);
+        for (int n = 0; n < 4; n += 2) {
+          uint32_t bh[4], bl[4];
+          frag_b<D>(bh, sm.c[0], 32 * wc + 8 * n, ks, lane);
+          frag_b<D>(bl, sm.c[1], 32 * wc + 8 * n, ks, lane);
+          mma16816_add(acc[n], ah, bh[0], bh[1]);
+          mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
+          mma16816(cross[n], ah, bl[0], bl[1]);
+          mma16816(cross[n + 1], ah, bl[2], bl[3]);
+          mma16816(cross[n], al, bh[0], bh[1]);
+          mma16816(cross[n + 1], al, bh[2], bh[3]);
         }
       }
     }
-  }
-  const int j = row0 + 4 * rq;             // RG is a multiple of 4: the four rows share a group
-  const int b = j / a.RP, rho = j % a.RP;
-  if (b < a.B) {
-    float* t = a.lut + (((int64_t)b * a.Hkv + kvh) * (a.RP / a.RG) + rho / a.RG) *
-                           ((int64_t)kCodebook * a.SKP * a.RG) + rho % a.RG;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float4 o;
-      o.x = acc[u][0] * a.scale_log2;
-      o.y = acc[u][1] * a.scale_log2;
-      o.z = acc[u][2] * a.scale_log2;
-      o.w = acc[u][3] * a.scale_log2;
-      *reinterpret_cast<float4*>(t + ((int64_t)(c0 + cc + 16 * u) * a.SKP + s) * a.RG) = o;
+    for (int q = 0; q < 2; ++q) {
+      if (!out[q]) continue;
+      const float qs = real ? sm.qs[16 * wr + g + 8 * q] : 0.f;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int cl = 32 * wc + 8 * n + 2 * t4 + i;
+          const float x = real ? (acc[n][2 * q + i] + cross[n][2 * q + i]) * sm.cs[cl] * qs : 0.f;
+          out[q][((int64_t)(c0 + chunk * kQtCodes + cl) * a.SKP + s) * a.RG] = x;
+        }
     }
   }
 }

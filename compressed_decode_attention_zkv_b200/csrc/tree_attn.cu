@@ -6,20 +6,21 @@
 // Innovations" (fp32 log-sum-exp combine).  The tree of drafts has no counterpart on the pages.
 //
 // A (sequence, kv head) pair has R = N * G query rows rho = i * G + g, taken in groups ("items")
-// of kTreeRG = 8.  Four kernels per call (programmatic dependent launches):
-//   1. tree_prepare_kernel  the key lookup tables of every row (query_tables.cuh); the dense part,
-//      one block per item (fp16 window and the drafts that the mask names: partial maximum, sum
-//      and output per row); one block computes the partition of the compressed tokens.
+// of kTreeRG = 8.  Five kernels per call (programmatic dependent launches):
+//   1. tree_dense_kernel    the dense part (fp16 window and the drafts that the mask names: partial
+//      maximum, sum and output per row); one block computes the partition of the compressed tokens.
+//      tree_tables_kernel   beside it: the key lookup tables of every row (query_tables.cuh).
 //   2. tree_scan_kernel     per item and range of tokens: base-2 scores from the tables and the
 //      per-codeword weight histograms W_s[c][row] = sum over the tokens with zv_s = c of
 //      2^(score - ref).  Each (range, item) writes one slot.
-//   3. tree_contract_kernel joins the slots of an item and contracts W_s with the value
-//      codebooks: one part per (stage, half of the codewords).
+//   3. tree_contract_kernel joins the slots of an item and contracts W_s with the value codebooks:
+//      one part per (stage, half of the codewords).
 //   4. tree_finish_kernel   sums the parts, rotates back, joins the dense part by log-sum-exp.
 #include "query_tables.cuh"
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 namespace zkv {
@@ -71,20 +72,25 @@ __device__ __forceinline__ int64_t comp_tokens(const int32_t* comp_len, int b, i
 // 1. Tables, dense part, partition
 // ---------------------------------------------------------------------------------------------
 
+constexpr int kTreeDenseThreads = 128;
+constexpr int kTreeDenseRows = 64;    // query rows of a dense block, 16 per warp
+constexpr int kTreeDenseKeys = 64;    // keys per step
+
 template <int D>
 struct TreeDenseSmem {
-  static constexpr int LD = D + 8;          // fp16 row stride: conflict-free 16-byte reads
-  float q[kTreeRG][D];
-  __half k[32 * LD];
-  __half v[32 * LD];
+  __half q[kTreeDenseRows * D];
+  __half k[kTreeDenseKeys * D];
+  __half v[kTreeDenseKeys * D];
+  int odd;                            // a draft's value holds an infinity or NaN
 };
 
 // prefix sums of the sequences' units and the range of one scan block (at least kTreeMinUnits)
 __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
-  __shared__ int64_t ws[kQtThreads / 32];
+  constexpr int T = kTreeDenseThreads;
+  __shared__ int64_t ws[T / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kQtThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += T) {
     const int b = b0 + tid;
     int64_t u = 0;
     if (b < a.B) {
@@ -104,7 +110,7 @@ __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
     if (lane == 31) ws[warp] = s;
     __syncthreads();
     int64_t before = base, all = 0;
-    for (int w = 0; w < kQtThreads / 32; ++w) {
+    for (int w = 0; w < T / 32; ++w) {
       if (w < warp) before += ws[w];
       all += ws[w];
     }
@@ -120,36 +126,57 @@ __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
   }
 }
 
-// Dense attention of one item: warp = row, lane = key in the scores, head dimensions in the output.
-template <int D>
-__device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t item, TreeDenseSmem<D>& sm) {
-  constexpr int E = D / 32, LD = TreeDenseSmem<D>::LD;
+// Dense attention of up to 64 rows of a pair over its window and its drafts: one pass over the keys
+// in steps of 64 with running maxima and sums.  4 / SPLIT warps take 16 rows each; with few rows
+// SPLIT warps share the keys of a step and are joined at the end.  Queries, keys and values are
+// fp16 and their products exact; the weights are split into two fp16 planes, and every 16 products
+// are added up in float32.
+template <int D, int SPLIT>
+__device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeDenseSmem<D>& sm) {
+  constexpr int NT = D / 8, NS = 8 / SPLIT;    // output and score tiles of 8 columns
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rg = (int)(item % a.NRG);
-  const int64_t pair = item / a.NRG;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int tiles = (a.R + kTreeDenseRows - 1) / kTreeDenseRows;
+  const int row0 = (int)(blk % tiles) * kTreeDenseRows;
+  const int64_t pair = blk / tiles;
   const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv);
   const int nd = present_queries(a.n_draft, b, a.N);
   int64_t wl = a.win_len[b];
   wl = wl < 0 ? 0 : wl > a.Wcap ? a.Wcap : wl;
-  const int rho = rg * kTreeRG + warp;
-  const int i = rho / a.G;
-  const bool live = rho < a.R && i < nd;
-  if ((rg * kTreeRG) / a.G >= nd) return;      // no row of the block is present (block-uniform)
+  if (row0 / a.G >= nd) return;                // no row of the block is present (block-uniform)
+  const int rows = a.R - row0 < kTreeDenseRows ? a.R - row0 : kTreeDenseRows;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int f = tid; f < (rows + 15) / 16 * 16 * (D / 8); f += kTreeDenseThreads) {
+    const int r = f / (D / 8), c = (f % (D / 8)) * 8, rho = row0 + r;
+    __half* dst = sm.q + tile_at<D>(r, c);
+    if (rho < a.R && rho / a.G < nd)
+      cp_async16(dst, a.qt.q + b * a.qt.q_sb + (rho / a.G) * a.qt.q_sn +
+                          ((int64_t)kvh * a.G + rho % a.G) * a.qt.q_sh + c);
+    else
+      *reinterpret_cast<uint4*>(dst) = zero;
+  }
+  const int wr = warp / SPLIT, ws = warp % SPLIT;   // the warp's row tile and share of the keys
+  const bool work = 16 * wr < rows;            // this warp has rows
+  int draft[2];                                // the draft of rows g and g + 8
+  const uint8_t* mrow[2];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    sm.q[warp][e * 32 + lane] =
-        live ? __half2float(a.qt.q[b * a.qt.q_sb + i * a.qt.q_sn +
-                                   ((int64_t)kvh * a.G + rho % a.G) * a.qt.q_sh + e * 32 + lane])
-             : 0.f;
+  for (int q = 0; q < 2; ++q) {
+    const int rho = row0 + 16 * wr + g + 8 * q;
+    draft[q] = rho < a.R && rho / a.G < nd ? rho / a.G : -1;
+    mrow[q] = a.mask ? a.mask + b * a.m_sb + (int64_t)(draft[q] < 0 ? 0 : draft[q]) * a.m_sn : nullptr;
+  }
+  float o[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
   const int64_t nk = wl + nd;
-  float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const uint8_t* mrow = a.mask ? a.mask + b * a.m_sb + (int64_t)(live ? i : 0) * a.m_sn : nullptr;
-  for (int64_t k0 = 0; k0 < nk; k0 += 32) {
-    __syncthreads();
-    for (int f = tid; f < 32 * (D / 8); f += kQtThreads) {
-      const int r = f / (D / 8), c = (f % (D / 8)) * 8;
+  for (int64_t k0 = 0; k0 < nk; k0 += kTreeDenseKeys) {
+    __syncthreads();                           // the previous keys have been read
+    if (tid == 0 && k0 == 0) sm.odd = 0;
+    for (int f = tid; f < kTreeDenseKeys * (D / 8); f += kTreeDenseThreads) {
+      const int r = f / (D / 8), c = (f % (D / 8)) * 8, at = tile_at<D>(r, c);
       const int64_t t = k0 + r;
       if (t < nk) {
         const __half *ks, *vs;
@@ -160,75 +187,215 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t item, Tree
           ks = a.dk + b * a.k_sb + (t - wl) * a.k_sn + (int64_t)kvh * a.k_sh;
           vs = a.dv + b * a.v_sb + (t - wl) * a.v_sn + (int64_t)kvh * a.v_sh;
         }
-        cp_async16(sm.k + r * LD + c, ks + c);
-        cp_async16(sm.v + r * LD + c, vs + c);
+        cp_async16(sm.k + at, ks + c);
+        cp_async16(sm.v + at, vs + c);
+      } else {
+        *reinterpret_cast<uint4*>(sm.k + at) = zero;
+        *reinterpret_cast<uint4*>(sm.v + at) = zero;
       }
     }
     cp_async_wait_all();
     __syncthreads();
-    const int64_t t = k0 + lane;
-    bool see = live && t < nk;
-    if (see && t >= wl) see = mrow ? mrow[t - wl] != 0 : t - wl <= i;
-    float s0 = 0.f, s1 = 0.f;
-    if (see) {
-#pragma unroll 4
-      for (int c = 0; c < D; c += 8) {
-        const uint4 kv = *reinterpret_cast<const uint4*>(sm.k + lane * LD + c);
-        const float4 qa = *reinterpret_cast<const float4*>(&sm.q[warp][c]);
-        const float4 qb = *reinterpret_cast<const float4*>(&sm.q[warp][c + 4]);
-        const float2 k01 = __half22float2(*reinterpret_cast<const __half2*>(&kv.x));
-        const float2 k23 = __half22float2(*reinterpret_cast<const __half2*>(&kv.y));
-        const float2 k45 = __half22float2(*reinterpret_cast<const __half2*>(&kv.z));
-        const float2 k67 = __half22float2(*reinterpret_cast<const __half2*>(&kv.w));
-        s0 = fmaf(qa.x, k01.x, s0); s1 = fmaf(qa.y, k01.y, s1);
-        s0 = fmaf(qa.z, k23.x, s0); s1 = fmaf(qa.w, k23.y, s1);
-        s0 = fmaf(qb.x, k45.x, s0); s1 = fmaf(qb.y, k45.y, s1);
-        s0 = fmaf(qb.z, k67.x, s0); s1 = fmaf(qb.w, k67.y, s1);
+    // a draft that a row does not see must not reach it through 0 * infinity: what is not finite is
+    // taken out of the products and added at the end to the rows that see it
+    if (k0 + kTreeDenseKeys > wl) {
+      for (int f = tid; f < kTreeDenseKeys * (D / 8); f += kTreeDenseThreads) {
+        uint4& x = *reinterpret_cast<uint4*>(sm.v + tile_at<D>(f / (D / 8), (f % (D / 8)) * 8));
+        uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        bool any = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if ((y[q] & 0x7c00u) == 0x7c00u) y[q] &= 0xffff0000u, any = true;
+          if ((y[q] & 0x7c000000u) == 0x7c000000u) y[q] &= 0xffffu, any = true;
+        }
+        if (any && k0 + f / (D / 8) >= wl) {
+          x = make_uint4(y[0], y[1], y[2], y[3]);
+          sm.odd = 1;
+        }
+      }
+      __syncthreads();
+    }
+    if (!work) continue;
+    const int key0 = ws * (64 / SPLIT);        // the warp's keys of the step
+    float s[NS][4];
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+#pragma unroll 2
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t qf[4];
+      frag_a<D>(qf, sm.q, 16 * wr, ks, lane);
+#pragma unroll
+      for (int n = 0; n < NS; n += 2) {
+        uint32_t kf[4];
+        frag_b<D>(kf, sm.k, key0 + 8 * n, ks, lane);
+        mma16816_add(s[n], qf, kf[0], kf[1]);
+        mma16816_add(s[n + 1], qf, kf[2], kf[3]);
       }
     }
-    const float x = see ? (s0 + s1) * a.qt.scale_log2 : -INFINITY;
-    unsigned keys = __ballot_sync(0xffffffffu, see);
-    if (!keys) continue;
-    const float mn = fmaxf(m, warp_max_f32(x));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float corr = ex2_approx(m - ref);
-    const float p = see ? ex2_approx(x - ref) : 0.f;
-    l = l * corr + warp_sum_f32(p);
-    m = mn;
+    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= corr;
-    while (keys) {      // a key that the row does not see is not multiplied: its value may be NaN
-      const int j = __ffs(keys) - 1;
-      keys &= keys - 1u;
-      const float w = __shfl_sync(0xffffffffu, p, j);
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        o[e] = fmaf(w, __half2float(sm.v[j * LD + e * 32 + lane]), o[e]);
+      for (int i = 0; i < 4; ++i) {
+        const int q = i >> 1;
+        const int64_t t = k0 + key0 + 8 * n + 2 * t4 + (i & 1);
+        bool see = draft[q] >= 0 && t < nk;
+        if (see && t >= wl) see = mrow[q] ? mrow[q][t - wl] != 0 : t - wl <= draft[q];
+        s[n][i] = see ? s[n][i] * a.qt.scale_log2 : -INFINITY;
+        mx[q] = fmaxf(mx[q], s[n][i]);
+      }
+    float ref[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      mx[q] = fmaxf(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], 1));
+      mx[q] = fmaxf(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], 2));
+      const float mn = fmaxf(m[q], mx[q]);
+      ref[q] = mn == -INFINITY ? 0.f : mn;
+      const float corr = ex2_approx(m[q] - ref[q]);
+      m[q] = mn;
+      l[q] *= corr;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        o[n][2 * q] *= corr;
+        o[n][2 * q + 1] *= corr;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[n][i] = ex2_approx(s[n][i] - ref[i >> 1]);
+        l[i >> 1] += s[n][i];
+      }
+#pragma unroll
+    for (int kk = 0; kk < kTreeDenseKeys / 16 / SPLIT; ++kk) {
+      // the weights of 16 keys as an A operand: high and low plane
+      uint32_t ph[4], pl[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = s[2 * kk + (i >> 1)][2 * (i & 1)], y = s[2 * kk + (i >> 1)][2 * (i & 1) + 1];
+        const __half2 hi = __floats2half2_rn(x, y);
+        const float2 back = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(x - back.x, y - back.y);
+        ph[i] = *reinterpret_cast<const uint32_t*>(&hi);
+        pl[i] = *reinterpret_cast<const uint32_t*>(&lo);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t vf[4];
+        frag_bt<D>(vf, sm.v, 8 * n, key0 / 16 + kk, lane);
+        float t[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(t, pl, vf[0], vf[1]);
+        mma16816(u, pl, vf[2], vf[3]);
+        mma16816(t, ph, vf[0], vf[1]);
+        mma16816(u, ph, vf[2], vf[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[n][i] += t[i];
+          o[n + 1][i] += u[i];
+        }
+      }
     }
   }
-  if (!live) return;
-  const int64_t row = pair * a.RP + rho;
-  if (lane == 0) {
-    a.dm[row] = m;
-    a.dl[row] = l;
-  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.dout[row * D + e * 32 + lane] = o[e];
+  for (int q = 0; q < 2; ++q) {
+    l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
+    l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
+  }
+  if constexpr (SPLIT > 1) {
+    // join the warps that share rows: outputs in the keys' and values' space, in their order
+    __shared__ float ml[4][16][2];
+    float* os = reinterpret_cast<float*>(sm.k);        // [4][16][D]
+    static_assert(offsetof(TreeDenseSmem<D>, v) == offsetof(TreeDenseSmem<D>, k) + sizeof(sm.k) &&
+                      sizeof(sm.k) + sizeof(sm.v) >= 4 * 16 * D * sizeof(float), "fits");
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = g + 8 * q;
+      if (t4 == 0) {
+        ml[warp][r][0] = m[q];
+        ml[warp][r][1] = l[q];
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(os + (warp * 16 + r) * D + 8 * n + 2 * t4) = make_float2(o[n][2 * q], o[n][2 * q + 1]);
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += 4) {
+      const int rho = row0 + r, w0 = r / 16 * SPLIT, x = r % 16;
+      if (rho / a.G >= nd) continue;
+      float top = -INFINITY, sum = 0.f, f[SPLIT], y[D / 32];
+#pragma unroll
+      for (int k = 0; k < SPLIT; ++k) top = fmaxf(top, ml[w0 + k][x][0]);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < SPLIT; ++k) {
+        f[k] = ex2_approx(ml[w0 + k][x][0] - (top == -INFINITY ? 0.f : top));
+        sum = fmaf(ml[w0 + k][x][1], f[k], sum);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          y[e] = fmaf(os[((w0 + k) * 16 + x) * D + e * 32 + lane], f[k], y[e]);
+      }
+      const int64_t row = pair * a.RP + rho;
+      if (lane == 0) {
+        a.dm[row] = top;
+        a.dl[row] = sum;
+      }
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) a.dout[row * D + e * 32 + lane] = y[e];
+    }
+  } else if (work) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (draft[q] < 0) continue;
+      const int64_t row = pair * a.RP + row0 + 16 * wr + g + 8 * q;
+      if (t4 == 0) {
+        a.dm[row] = m[q];
+        a.dl[row] = l[q];
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(a.dout + row * D + 8 * n + 2 * t4) = make_float2(o[n][2 * q], o[n][2 * q + 1]);
+    }
+  }
+  __syncthreads();
+  if (!sm.odd) return;
+  for (int r = warp; r < rows; r += 4) {
+    const int i = (row0 + r) / a.G;
+    if (i >= nd) break;
+    for (int key = 0; key < nd; ++key) {
+      if (a.mask ? a.mask[b * a.m_sb + i * a.m_sn + key] == 0 : key > i) continue;
+      const __half* vs = a.dv + b * a.v_sb + key * a.v_sn + (int64_t)kvh * a.v_sh;
+      for (int c = lane; c < D; c += 32) {
+        const float v = __half2float(vs[c]);
+        if (!(fabsf(v) < INFINITY)) a.dout[(pair * a.RP + row0 + r) * D + c] += v;
+      }
+    }
+  }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kQtThreads) tree_prepare_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(kTreeDenseThreads) tree_dense_kernel(TreeArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   pdl_trigger();
-  int64_t blk = blockIdx.x;
-  const int64_t nt = a.qt.blocks();
-  if (blk < nt) {
-    query_tables_block<D>(a.qt, blk, *reinterpret_cast<QtSmem<D>*>(smraw));
-  } else if (blk == nt) {
-    tree_partition(a);
-  } else {
-    tree_dense<D>(a, blk - nt - 1, *reinterpret_cast<TreeDenseSmem<D>*>(smraw));
-  }
+  TreeDenseSmem<D>& sm = *reinterpret_cast<TreeDenseSmem<D>*>(smraw);
+  const int64_t blk = (int64_t)blockIdx.x - 1;
+  if (blk < 0) tree_partition(a);
+  else if (a.R <= 16) tree_dense<D, 4>(a, blk, sm);
+  else if (a.R <= 32) tree_dense<D, 2>(a, blk, sm);
+  else tree_dense<D, 1>(a, blk, sm);
+}
+
+// Runs beside the dense part, which it does not read, and completes after it.
+template <int D>
+__global__ void __launch_bounds__(kQtThreads) tree_tables_kernel(TreeArgs a) {
+  extern __shared__ __align__(16) unsigned char smraw[];
+  pdl_trigger();
+  query_tables_block<D>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D>*>(smraw));
+  pdl_wait();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -551,7 +718,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     auto tile_max = [&](uint32_t tile, int q, float (&x)[2]) {
       float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll 1
-      for (int k = 0; k < kTreeTK / 4; ++k) {
+      for (int k = 0; k < kTreeTK / 4 && tile + (k * C::NW + warp) * 32 < tend; ++k) {
         uint32_t w[4][C::KW];
         key_codes(std::false_type{}, q, k, w);
 #pragma unroll
@@ -569,6 +736,11 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       const float2 neg = make_float2(-ref[0], -ref[1]);
 #pragma unroll
       for (int k = 0; k < kTreeTK / 4; ++k) {
+        if (!FULL && tile + (k * C::NW + warp) * 32 >= tend) {     // none of the warp's tokens left
+#pragma unroll
+          for (int u = 0; u < 4; ++u) p[4 * k + u] = make_float2(0.f, 0.f);
+          continue;
+        }
         uint32_t w[4][C::KW];
         key_codes(full, q, k, w);
 #pragma unroll
@@ -582,9 +754,10 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       }
       return sum;
     };
-    auto tile_add = [&](auto ex, int q, const float2 (&p)[kTreeTK], const float (&mul)[2]) {
+    auto tile_add = [&](auto ex, uint32_t tile, int q, const float2 (&p)[kTreeTK], const float (&mul)[2]) {
 #pragma unroll
       for (int k = 0; k < kTreeTK / 4; ++k) {
+        if (tile + (k * C::NW + warp) * 32 >= tend) break;
         uint32_t w[4][C::VW];
         value_codes(ex, q, k, w);
 #pragma unroll
@@ -668,8 +841,8 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
         used[j] += sum[j] * mul[j] + (float)(C::TILE / 2);
       }
       dirty = true;
-      if (exact) tile_add(std::true_type{}, q, p, mul);
-      else tile_add(std::false_type{}, q, p, mul);
+      if (exact) tile_add(std::true_type{}, tile, q, p, mul);
+      else tile_add(std::false_type{}, tile, q, p, mul);
       __syncwarp();        // every lane has read the codes
     }
     __syncthreads();
@@ -686,44 +859,78 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
 // ---------------------------------------------------------------------------------------------
 // 3. Contraction with the value codebooks
 // ---------------------------------------------------------------------------------------------
-// Block = 8 items of one kv head (64 rows) x one chunk of codewords of one stage.  Warp = item in
-// both steps: it joins the item's slots by their references, then multiplies its 8 rows with the
-// block's codewords (lane = D / 32 head dimensions).
+// Block = 8 items of one kv head (64 rows) x 128 codewords of one stage: a product
+// [64 rows] x [128 codewords] x [D] with float32 accuracy (mma_split.cuh).  The codewords are read
+// and split before the wait for the scan.  Warp = item while the slots are joined by their
+// references; a weight takes over the power of two of its codeword, then each row is split.  In the
+// product 4 x 2 warps take 16 rows x D / 2 dimensions.
 template <int D>
 struct TreeContractSmem {
-  float cv[kTreeCw][D];
-  float w[8][kTreeCw][kTreeRG];
+  __half cv[2][kTreeCw * D];        // codewords [c][D], high and low plane
+  __half w[2][kTreeCw * 64];        // weights [c][64 rows]
+  float cs[kTreeCw];                // 2^e of the codewords
+  float ws[64];                     // 2^e of the rows
+  int64_t row[8];                   // first row of each item, -1: nothing to write
 };
 
 template <int D>
-__global__ void __launch_bounds__(256) tree_contract_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(TreeArgs a) {
   constexpr int E = D / 32;
   extern __shared__ __align__(16) unsigned char smraw[];
   TreeContractSmem<D>& sm = *reinterpret_cast<TreeContractSmem<D>*>(smraw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = blockIdx.x % (a.Sv * kTreeHalves);
+  const int parts = a.Sv * kTreeHalves, part = blockIdx.x % parts;
   const int s = part / kTreeHalves, half = part % kTreeHalves;
   const int kvh = blockIdx.y;
-  const int64_t j = (int64_t)(blockIdx.x / (a.Sv * kTreeHalves)) * 8 + warp;   // (b, rg) of kvh
+  const int64_t group = blockIdx.x / parts;
+  const int64_t j = group * 8 + warp;          // (b, rg) of kvh
   pdl_trigger();
   {
-    const float* cv = a.Cv + (((int64_t)kvh * a.Sv + s) * kCodebook + half * kTreeCw) * D;
-    float* dst = &sm.cv[0][0];
-    for (int f = tid; f < kTreeCw * D / 4; f += 256) cp_async16(dst + 4 * f, cv + 4 * f);
-    cp_async_commit();
+    // warp w splits codewords w, w + 8, ...; lane = E dimensions in a row
+    const float* C = a.Cv + (((int64_t)kvh * a.Sv + s) * kCodebook + half * kTreeCw) * D + lane * E;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kTreeCw / 8; k0 += 8) {
+      float v[8][E];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = __ldg(C + (int64_t)(8 * (k0 + k) + warp) * D + e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = 8 * (k0 + k) + warp;
+        float big = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[k][e]));
+        const int ex = split_exponent(warp_max_f32(big));
+        const float down = exp2_int(-ex);
+        if (lane == 0) sm.cs[c] = exp2_int(ex);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          alignas(4) __half hi[2], lo[2];
+          split(v[k][e] * down, hi[0], lo[0]);
+          split(v[k][e + 1] * down, hi[1], lo[1]);
+          const int at = tile_at<D>(c, lane * E + e);
+          *reinterpret_cast<uint32_t*>(sm.cv[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
+          *reinterpret_cast<uint32_t*>(sm.cv[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
+        }
+      }
+    }
   }
+  __syncthreads();
   pdl_wait();
   const bool live = j < (int64_t)a.B * a.NRG;
-  int64_t n = 0, row = 0;
-  if (live) {
-    const int b = (int)(j / a.NRG), rg = (int)(j % a.NRG);
-    const int64_t items_per_b = (int64_t)a.Hkv * a.NRG, in_b = (int64_t)kvh * a.NRG + rg;
-    const int64_t units = a.pre[b + 1] - a.pre[b], per = a.pre[a.B + 1];
-    const int64_t p0 = a.pre[b] * items_per_b + in_b * units;
-    const int64_t first = p0 / per;
-    n = units ? (p0 + units - 1) / per - first + 1 : 0;
-    const int64_t slot0 = b * items_per_b + in_b + first;
-    row = ((int64_t)b * a.Hkv + kvh) * a.RP + rg * kTreeRG;
+  {
+    int64_t n = 0, row = -1, slot0 = 0;
+    if (live) {
+      const int b = (int)(j / a.NRG), rg = (int)(j % a.NRG);
+      const int64_t items_per_b = (int64_t)a.Hkv * a.NRG, in_b = (int64_t)kvh * a.NRG + rg;
+      const int64_t units = a.pre[b + 1] - a.pre[b], per = a.pre[a.B + 1];
+      const int64_t p0 = a.pre[b] * items_per_b + in_b * units;
+      const int64_t first = p0 / per;
+      n = units ? (p0 + units - 1) / per - first + 1 : 0;
+      slot0 = b * items_per_b + in_b + first;
+      row = ((int64_t)b * a.Hkv + kvh) * a.RP + rg * kTreeRG;
+    }
     // lane holds rows r4 .. r4 + 3 of codewords lane / 2 + 16 k
     const int r4 = 4 * (lane & 1);
     float m[4];
@@ -736,112 +943,159 @@ __global__ void __launch_bounds__(256) tree_contract_kernel(TreeArgs a) {
       m[2] = fmaxf(m[2], x.z); m[3] = fmaxf(m[3], x.w);
       nan[0] |= x.x != x.x; nan[1] |= x.y != x.y; nan[2] |= x.z != x.z; nan[3] |= x.w != x.w;
     }
-    float4 acc[kTreeCw / 16];
+    float acc[kTreeCw / 16][4];
 #pragma unroll
-    for (int k = 0; k < kTreeCw / 16; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < kTreeCw / 16; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[k][q] = 0.f;
+#pragma unroll 2
     for (int64_t k = 0; k < n; ++k) {
       const float4 x = *reinterpret_cast<const float4*>(a.pm + (slot0 + k) * kTreeRG + r4);
-      const float4 f = make_float4(ex2_approx(x.x - m[0]), ex2_approx(x.y - m[1]),
-                                   ex2_approx(x.z - m[2]), ex2_approx(x.w - m[3]));
+      const float f[4] = {ex2_approx(x.x - m[0]), ex2_approx(x.y - m[1]), ex2_approx(x.z - m[2]),
+                          ex2_approx(x.w - m[3])};
       const float4* src = reinterpret_cast<const float4*>(
                               a.pw + (((slot0 + k) * a.Sv + s) * kCodebook + half * kTreeCw) * (int64_t)kTreeRG) + lane;
 #pragma unroll
       for (int c = 0; c < kTreeCw / 16; ++c) {
         const float4 v = src[32 * c];
-        acc[c].x = fmaf(f.x, v.x, acc[c].x);
-        acc[c].y = fmaf(f.y, v.y, acc[c].y);
-        acc[c].z = fmaf(f.z, v.z, acc[c].z);
-        acc[c].w = fmaf(f.w, v.w, acc[c].w);
+        acc[c][0] = fmaf(f[0], v.x, acc[c][0]);
+        acc[c][1] = fmaf(f[1], v.y, acc[c][1]);
+        acc[c][2] = fmaf(f[2], v.z, acc[c][2]);
+        acc[c][3] = fmaf(f[3], v.w, acc[c][3]);
       }
     }
-    float l[4] = {0.f, 0.f, 0.f, 0.f};
+    float l[4] = {0.f, 0.f, 0.f, 0.f}, big[4] = {0.f, 0.f, 0.f, 0.f}, down[4];
 #pragma unroll
     for (int c = 0; c < kTreeCw / 16; ++c) {
-      reinterpret_cast<float4*>(&sm.w[warp][0][0])[32 * c + lane] = acc[c];
-      l[0] += acc[c].x; l[1] += acc[c].y; l[2] += acc[c].z; l[3] += acc[c].w;
-    }
-    if (s == 0) {
-      // every token is counted once per stage: the sum of stage 0's weights is the row's sum
+      const float cs = sm.cs[16 * c + (lane >> 1)];
 #pragma unroll
-      for (int o = 2; o < 32; o <<= 1)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) l[q] += __shfl_xor_sync(0xffffffffu, l[q], o);
-      if (lane < 2) {
-        const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          a.rl[half * rows + row + r4 + q] = l[q];
-          if (half == 0) a.rm[row + r4 + q] = nan[q] ? NAN : m[q];
-        }
+      for (int q = 0; q < 4; ++q) {
+        l[q] += acc[c][q];
+        acc[c][q] *= cs;
+        big[q] = fmaxf(big[q], fabsf(acc[c][q]));
       }
     }
+    // sums and maxima over the lanes with the same rows
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        l[q] += __shfl_xor_sync(0xffffffffu, l[q], o);
+        big[q] = fmaxf(big[q], __shfl_xor_sync(0xffffffffu, big[q], o));
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int ex = split_exponent(big[q]);
+      down[q] = exp2_int(-ex);
+      if (lane < 2) sm.ws[8 * warp + r4 + q] = exp2_int(ex);
+    }
+    if (live && s == 0 && lane < 2) {
+      // every token is counted once per stage: the sum of stage 0's weights is the row's sum
+      const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        a.rl[half * rows + row + r4 + q] = l[q];
+        if (half == 0) a.rm[row + r4 + q] = nan[q] ? NAN : m[q];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kTreeCw / 16; ++c) {
+      alignas(8) __half hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) split(acc[c][q] * down[q], hi[q], lo[q]);
+      const int at = tile_at<64>(16 * c + (lane >> 1), 8 * warp + r4);
+      *reinterpret_cast<uint2*>(sm.w[0] + at) = *reinterpret_cast<const uint2*>(hi);
+      *reinterpret_cast<uint2*>(sm.w[1] + at) = *reinterpret_cast<const uint2*>(lo);
+    }
+    if (lane == 0) sm.row[warp] = n ? row : -1;
   }
-  cp_async_wait_all();
   __syncthreads();
-  if (!live || n == 0) return;
-  float o[kTreeRG][E];
+  const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
+  const int wr = warp & 3, wc = warp >> 2, g = lane >> 2, t4 = lane & 3;
+  if (sm.row[2 * wr] >= 0 || sm.row[2 * wr + 1] >= 0) {
+    constexpr int NT = D / 16;                 // output tiles of 8 dimensions
+    float acc[NT][4], cross[NT][4];
 #pragma unroll
-  for (int q = 0; q < kTreeRG; ++q)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[q][e] = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < kTreeCw; ++c) {
-    const float4 wa = *reinterpret_cast<const float4*>(&sm.w[warp][c][0]);
-    const float4 wb = *reinterpret_cast<const float4*>(&sm.w[warp][c][4]);
-    const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+      for (int i = 0; i < 4; ++i) acc[n][i] = cross[n][i] = 0.f;
+#pragma unroll 1
+    for (int ks = 0; ks < kTreeCw / 16; ++ks) {
+      uint32_t ah[4], al[4];
+      frag_at<64>(ah, sm.w[0], 16 * wr, ks, lane);
+      frag_at<64>(al, sm.w[1], 16 * wr, ks, lane);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float v = sm.cv[c][e * 32 + lane];
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t bh[4], bl[4];
+        frag_bt<D>(bh, sm.cv[0], wc * (D / 2) + 8 * n, ks, lane);
+        frag_bt<D>(bl, sm.cv[1], wc * (D / 2) + 8 * n, ks, lane);
+        mma16816_add(acc[n], ah, bh[0], bh[1]);
+        mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
+        mma16816(cross[n], ah, bl[0], bl[1]);
+        mma16816(cross[n + 1], ah, bl[2], bl[3]);
+        mma16816(cross[n], al, bh[0], bh[1]);
+        mma16816(cross[n + 1], al, bh[2], bh[3]);
+      }
+    }
 #pragma unroll
-      for (int q = 0; q < kTreeRG; ++q) o[q][e] = fmaf(w[q], v, o[q][e]);
+    for (int q = 0; q < 2; ++q) {
+      const int64_t row = sm.row[2 * wr + q];
+      if (row < 0) continue;
+      const float ws = sm.ws[16 * wr + 8 * q + g];
+      float* o = a.parts + (part * rows + row + g) * D + wc * (D / 2) + 2 * t4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(o + 8 * n) = make_float2((acc[n][2 * q] + cross[n][2 * q]) * ws,
+                                                            (acc[n][2 * q + 1] + cross[n][2 * q + 1]) * ws);
     }
   }
-  const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
-#pragma unroll
-  for (int q = 0; q < kTreeRG; ++q)
-#pragma unroll
-    for (int e = 0; e < E; ++e) a.parts[(part * rows + row + q) * D + e * 32 + lane] = o[q][e];
 }
 
 // ---------------------------------------------------------------------------------------------
-// 4. Sum of the parts, rotation back, join with the dense part: one warp per row
+// 4. Sum of the parts in their order, rotation back, join with the dense part: one warp per row
 // ---------------------------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(256) tree_finish_kernel(TreeArgs a) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(128) tree_finish_kernel(TreeArgs a) {
+  constexpr int E = D / 32, W = 4;             // dimensions per lane; warps
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  const int64_t x = (int64_t)blockIdx.x * 8 + warp;      // (pair, rho)
+  const int64_t x = (int64_t)blockIdx.x * W + warp;      // (pair, rho)
   const int64_t pair = x / a.R;
   const int rho = (int)(x % a.R);
+  pdl_wait();
   if (pair >= (int64_t)a.B * a.Hkv) return;
   const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv), i = rho / a.G;
   if (i >= present_queries(a.n_draft, b, a.N)) return;   // rows behind the drafts stay as they are
   const int64_t rows = (int64_t)a.B * a.Hkv * a.RP, row = pair * a.RP + rho;
-  const float m = a.rm[row], dm = a.dm[row];
+  const float m = a.rm[row], dm = a.dm[row], dl = a.dl[row];
   float l = a.rl[row];
 #pragma unroll
   for (int k = 1; k < kTreeHalves; ++k) l += a.rl[k * rows + row];
-  float o[E];
+  float o[E], y[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int e = 0; e < E; ++e) {
+    o[e] = 0.f;
+    y[e] = a.dout[row * D + e * 32 + lane];
+  }
   if (m != -INFINITY) {
-    for (int p = 0; p < a.Sv * kTreeHalves; ++p)
+    static_assert(kTreeHalves == 2, "two parts per stage");
+#pragma unroll 4
+    for (int p = 0; p < a.Sv; ++p)
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += a.parts[(p * rows + row) * D + e * 32 + lane];
+      for (int e = 0; e < E; ++e)
+        o[e] += a.parts[(2 * p * rows + row) * D + e * 32 + lane] +
+                a.parts[((2 * p + 1) * rows + row) * D + e * 32 + lane];
     fwht_warp_f32<D>(o, lane);
   }
-  const float M = fmaxf(m, dm), top = M == -INFINITY ? 0.f : M;
+  const float M = m != m ? m : fmaxf(m, dm), top = M == -INFINITY ? 0.f : M;
   const float fc = ex2_approx(m - top), fd = ex2_approx(dm - top);
-  const float total = l * fc + a.dl[row] * fd;
+  const float total = l * fc + dl * fd;
   const bool none = total == 0.f;
   const float inv = none ? 0.f : 1.f / total;
   const float gc = fc * inv * (float)a.qt.rot, gd = fd * inv;
   const int64_t at = ((int64_t)b * a.N + i) * a.Hq + (int64_t)kvh * a.G + rho % a.G;
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    a.out[at * D + e * 32 + lane] =
-        none ? 0.f : fmaf(o[e], gc, a.dout[row * D + e * 32 + lane] * gd);
+    a.out[at * D + e * 32 + lane] = none ? 0.f : fmaf(o[e], gc, y[e] * gd);
   if (a.lse && lane == 0) a.lse[at] = none ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
@@ -946,15 +1200,18 @@ static cudaError_t launch_tree_scan_v(const TreeArgs& a, int SVP, cudaStream_t s
 
 template <int D>
 static int launch_tree(const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
-  const size_t s1 = std::max(sizeof(QtSmem<D>), sizeof(TreeDenseSmem<D>));
-  const size_t s3 = sizeof(TreeContractSmem<D>);
-  static_assert(sizeof(QtSmem<D>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax, "fits");
-  if (ensure_smem_limit(tree_prepare_kernel<D>, s1) != cudaSuccess ||
+  const size_t s0 = sizeof(TreeDenseSmem<D>), s1 = sizeof(QtSmem<D>), s3 = sizeof(TreeContractSmem<D>);
+  static_assert(sizeof(QtSmem<D>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax &&
+                    sizeof(TreeDenseSmem<D>) <= kTreeSmemMax, "fits");
+  if (ensure_smem_limit(tree_dense_kernel<D>, s0) != cudaSuccess ||
+      ensure_smem_limit(tree_tables_kernel<D>, s1) != cudaSuccess ||
       ensure_smem_limit(tree_contract_kernel<D>, s3) != cudaSuccess)
     return ZKV_ERR_CUDA;
-  const int64_t b1 = a.qt.blocks() + 1 + t.items;
-  tree_prepare_kernel<D><<<(unsigned)b1, kQtThreads, s1, st>>>(a);
+  const int64_t b0 = 1 + (int64_t)a.B * a.Hkv * ((a.R + kTreeDenseRows - 1) / kTreeDenseRows);
+  tree_dense_kernel<D><<<(unsigned)b0, kTreeDenseThreads, s0, st>>>(a);
   ZKV_CHECK_LAUNCH();
+  if (launch_pdl(tree_tables_kernel<D>, dim3((unsigned)a.qt.blocks()), dim3(kQtThreads), s1, st, a) != cudaSuccess)
+    return ZKV_ERR_CUDA;
   cudaError_t e;
   switch (t.SKP) {
     case 1: e = launch_tree_scan_v<1>(a, t.SVP, st); break;
@@ -968,8 +1225,7 @@ static int launch_tree(const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
                  s3, st, a) != cudaSuccess)
     return ZKV_ERR_CUDA;
   const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
-  if (launch_pdl(tree_finish_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a) !=
-      cudaSuccess)
+  if (launch_pdl(tree_finish_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a) != cudaSuccess)
     return ZKV_ERR_CUDA;
   return ZKV_OK;
 }
