@@ -34,10 +34,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// d += a b with the 16 terms summed from zero and added in float32
+__device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+               "{%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// d = a b; d += a b with the 16 terms summed from zero and added in float32
 __device__ __forceinline__ void mma16816_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
-  mma16816(t, a, b0, b1);
+  float t[4];
+  mma16816_zero(t, a, b0, b1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) d[i] += t[i];
 }

@@ -73,15 +73,17 @@ __device__ __forceinline__ int64_t comp_tokens(const int32_t* comp_len, int b, i
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kTreeDenseThreads = 128;
-constexpr int kTreeDenseRows = 64;    // query rows of a dense block, 16 per warp
-constexpr int kTreeDenseKeys = 64;    // keys per step
+constexpr int kTreeDenseRows = 16;    // query rows of a dense block
+constexpr int kTreeDenseKeys = 64;    // keys per step, 16 per warp
 
 template <int D>
 struct TreeDenseSmem {
   __half q[kTreeDenseRows * D];
   __half k[kTreeDenseKeys * D];
   __half v[kTreeDenseKeys * D];
-  int odd;                            // a draft's value holds an infinity or NaN
+  unsigned long long see[kTreeDenseRows];   // the keys of the step that a row attends to
+  float ml[4][kTreeDenseRows][2];           // maximum and sum of each warp's keys
+  int odd;                                  // a draft's value holds an infinity or NaN
 };
 
 // prefix sums of the sequences' units and the range of one scan block (at least kTreeMinUnits)
@@ -126,14 +128,13 @@ __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
   }
 }
 
-// Dense attention of up to 64 rows of a pair over its window and its drafts: one pass over the keys
-// in steps of 64 with running maxima and sums.  4 / SPLIT warps take 16 rows each; with few rows
-// SPLIT warps share the keys of a step and are joined at the end.  Queries, keys and values are
-// fp16 and their products exact; the weights are split into two fp16 planes, and every 16 products
-// are added up in float32.
-template <int D, int SPLIT>
+// Dense attention of 16 rows of a pair over its window and its drafts: one pass over the keys in
+// steps of 64, 16 keys per warp with running maxima and sums of the warp's own; the four warps are
+// joined at the end.  Queries, keys and values are fp16 and their products exact; the weights are
+// split into two fp16 planes, and every 16 products are added up in float32.
+template <int D>
 __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeDenseSmem<D>& sm) {
-  constexpr int NT = D / 8, NS = 8 / SPLIT;    // output and score tiles of 8 columns
+  constexpr int NT = D / 8;                    // output tiles of 8 columns
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int tiles = (a.R + kTreeDenseRows - 1) / kTreeDenseRows;
@@ -144,9 +145,8 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
   int64_t wl = a.win_len[b];
   wl = wl < 0 ? 0 : wl > a.Wcap ? a.Wcap : wl;
   if (row0 / a.G >= nd) return;                // no row of the block is present (block-uniform)
-  const int rows = a.R - row0 < kTreeDenseRows ? a.R - row0 : kTreeDenseRows;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int f = tid; f < (rows + 15) / 16 * 16 * (D / 8); f += kTreeDenseThreads) {
+  for (int f = tid; f < kTreeDenseRows * (D / 8); f += kTreeDenseThreads) {
     const int r = f / (D / 8), c = (f % (D / 8)) * 8, rho = row0 + r;
     __half* dst = sm.q + tile_at<D>(r, c);
     if (rho < a.R && rho / a.G < nd)
@@ -155,17 +155,7 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
     else
       *reinterpret_cast<uint4*>(dst) = zero;
   }
-  const int wr = warp / SPLIT, ws = warp % SPLIT;   // the warp's row tile and share of the keys
-  const bool work = 16 * wr < rows;            // this warp has rows
-  int draft[2];                                // the draft of rows g and g + 8
-  const uint8_t* mrow[2];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int rho = row0 + 16 * wr + g + 8 * q;
-    draft[q] = rho < a.R && rho / a.G < nd ? rho / a.G : -1;
-    mrow[q] = a.mask ? a.mask + b * a.m_sb + (int64_t)(draft[q] < 0 ? 0 : draft[q]) * a.m_sn : nullptr;
-  }
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};     // rows g and g + 8
   float o[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -194,6 +184,24 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
         *reinterpret_cast<uint4*>(sm.v + at) = zero;
       }
     }
+    cp_async_commit();
+    // warp w finds the keys that rows 4 w .. 4 w + 3 attend to
+    bool see[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int rho = row0 + 4 * warp + r, i = rho / a.G;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int64_t t = k0 + 32 * q + lane, x = t - wl;
+        see[r][q] = rho < a.R && i < nd && t < nk;
+        if (see[r][q] && x >= 0) see[r][q] = a.mask ? a.mask[b * a.m_sb + i * a.m_sn + x] != 0 : x <= i;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const unsigned lo = __ballot_sync(0xffffffffu, see[r][0]), hi = __ballot_sync(0xffffffffu, see[r][1]);
+      if (lane == 0) sm.see[4 * warp + r] = (unsigned long long)hi << 32 | lo;
+    }
     cp_async_wait_all();
     __syncthreads();
     // a draft that a row does not see must not reach it through 0 * infinity: what is not finite is
@@ -215,36 +223,31 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
       }
       __syncthreads();
     }
-    if (!work) continue;
-    const int key0 = ws * (64 / SPLIT);        // the warp's keys of the step
-    float s[NS][4];
+    uint32_t bits[2];
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int q = 0; q < 2; ++q) bits[q] = (uint32_t)(sm.see[g + 8 * q] >> (16 * warp)) & 0xffffu;
+    if (!__any_sync(0xffffffffu, bits[0] | bits[1])) continue;
+    float s[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
-#pragma unroll 2
-    for (int ks = 0; ks < D / 16; ++ks) {
-      uint32_t qf[4];
-      frag_a<D>(qf, sm.q, 16 * wr, ks, lane);
 #pragma unroll
-      for (int n = 0; n < NS; n += 2) {
-        uint32_t kf[4];
-        frag_b<D>(kf, sm.k, key0 + 8 * n, ks, lane);
-        mma16816_add(s[n], qf, kf[0], kf[1]);
-        mma16816_add(s[n + 1], qf, kf[2], kf[3]);
-      }
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t qf[4], kf[4];
+      frag_a<D>(qf, sm.q, 0, ks, lane);
+      frag_b<D>(kf, sm.k, 16 * warp, ks, lane);
+      mma16816_add(s[0], qf, kf[0], kf[1]);
+      mma16816_add(s[1], qf, kf[2], kf[3]);
     }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int q = i >> 1;
-        const int64_t t = k0 + key0 + 8 * n + 2 * t4 + (i & 1);
-        bool see = draft[q] >= 0 && t < nk;
-        if (see && t >= wl) see = mrow[q] ? mrow[q][t - wl] != 0 : t - wl <= draft[q];
-        s[n][i] = see ? s[n][i] * a.qt.scale_log2 : -INFINITY;
-        mx[q] = fmaxf(mx[q], s[n][i]);
+        const bool sees = bits[i >> 1] >> (8 * n + 2 * t4 + (i & 1)) & 1u;
+        s[n][i] = sees ? s[n][i] * a.qt.scale_log2 : -INFINITY;
+        mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
       }
     float ref[2];
 #pragma unroll
@@ -262,118 +265,87 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
         o[n][2 * q + 1] *= corr;
       }
     }
+    // the weights of the warp's 16 keys as an A operand: high and low plane
+    uint32_t ph[4], pl[4];
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
+    for (int i = 0; i < 4; ++i) {
+      const float x = ex2_approx(s[i >> 1][2 * (i & 1)] - ref[i & 1]);
+      const float y = ex2_approx(s[i >> 1][2 * (i & 1) + 1] - ref[i & 1]);
+      l[i & 1] += x + y;
+      const __half2 hi = __floats2half2_rn(x, y);
+      const float2 back = __half22float2(hi);
+      const __half2 lo = __floats2half2_rn(x - back.x, y - back.y);
+      ph[i] = *reinterpret_cast<const uint32_t*>(&hi);
+      pl[i] = *reinterpret_cast<const uint32_t*>(&lo);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      uint32_t vf[4];
+      frag_bt<D>(vf, sm.v, 8 * n, warp, lane);
+      float t[4], u[4];
+      mma16816_zero(t, pl, vf[0], vf[1]);
+      mma16816_zero(u, pl, vf[2], vf[3]);
+      mma16816(t, ph, vf[0], vf[1]);
+      mma16816(u, ph, vf[2], vf[3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[n][i] = ex2_approx(s[n][i] - ref[i >> 1]);
-        l[i >> 1] += s[n][i];
-      }
-#pragma unroll
-    for (int kk = 0; kk < kTreeDenseKeys / 16 / SPLIT; ++kk) {
-      // the weights of 16 keys as an A operand: high and low plane
-      uint32_t ph[4], pl[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = s[2 * kk + (i >> 1)][2 * (i & 1)], y = s[2 * kk + (i >> 1)][2 * (i & 1) + 1];
-        const __half2 hi = __floats2half2_rn(x, y);
-        const float2 back = __half22float2(hi);
-        const __half2 lo = __floats2half2_rn(x - back.x, y - back.y);
-        ph[i] = *reinterpret_cast<const uint32_t*>(&hi);
-        pl[i] = *reinterpret_cast<const uint32_t*>(&lo);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t vf[4];
-        frag_bt<D>(vf, sm.v, 8 * n, key0 / 16 + kk, lane);
-        float t[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(t, pl, vf[0], vf[1]);
-        mma16816(u, pl, vf[2], vf[3]);
-        mma16816(t, ph, vf[0], vf[1]);
-        mma16816(u, ph, vf[2], vf[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[n][i] += t[i];
-          o[n + 1][i] += u[i];
-        }
+        o[n][i] += t[i];
+        o[n + 1][i] += u[i];
       }
     }
   }
+  // join the warps, in their order
+  float* os = reinterpret_cast<float*>(sm.k);          // [4][16][D]
+  static_assert(offsetof(TreeDenseSmem<D>, v) == offsetof(TreeDenseSmem<D>, k) + sizeof(sm.k) &&
+                    sizeof(sm.k) + sizeof(sm.v) >= 4 * kTreeDenseRows * D * sizeof(float), "fits");
+  __syncthreads();
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
+    const int r = g + 8 * q;
     l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
     l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
-  }
-  if constexpr (SPLIT > 1) {
-    // join the warps that share rows: outputs in the keys' and values' space, in their order
-    __shared__ float ml[4][16][2];
-    float* os = reinterpret_cast<float*>(sm.k);        // [4][16][D]
-    static_assert(offsetof(TreeDenseSmem<D>, v) == offsetof(TreeDenseSmem<D>, k) + sizeof(sm.k) &&
-                      sizeof(sm.k) + sizeof(sm.v) >= 4 * 16 * D * sizeof(float), "fits");
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int r = g + 8 * q;
-      if (t4 == 0) {
-        ml[warp][r][0] = m[q];
-        ml[warp][r][1] = l[q];
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(os + (warp * 16 + r) * D + 8 * n + 2 * t4) = make_float2(o[n][2 * q], o[n][2 * q + 1]);
+    if (t4 == 0) {
+      sm.ml[warp][r][0] = m[q];
+      sm.ml[warp][r][1] = l[q];
     }
-    __syncthreads();
-    for (int r = warp; r < rows; r += 4) {
-      const int rho = row0 + r, w0 = r / 16 * SPLIT, x = r % 16;
-      if (rho / a.G >= nd) continue;
-      float top = -INFINITY, sum = 0.f, f[SPLIT], y[D / 32];
 #pragma unroll
-      for (int k = 0; k < SPLIT; ++k) top = fmaxf(top, ml[w0 + k][x][0]);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < SPLIT; ++k) {
-        f[k] = ex2_approx(ml[w0 + k][x][0] - (top == -INFINITY ? 0.f : top));
-        sum = fmaf(ml[w0 + k][x][1], f[k], sum);
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-          y[e] = fmaf(os[((w0 + k) * 16 + x) * D + e * 32 + lane], f[k], y[e]);
-      }
-      const int64_t row = pair * a.RP + rho;
-      if (lane == 0) {
-        a.dm[row] = top;
-        a.dl[row] = sum;
-      }
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) a.dout[row * D + e * 32 + lane] = y[e];
-    }
-  } else if (work) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (draft[q] < 0) continue;
-      const int64_t row = pair * a.RP + row0 + 16 * wr + g + 8 * q;
-      if (t4 == 0) {
-        a.dm[row] = m[q];
-        a.dl[row] = l[q];
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(a.dout + row * D + 8 * n + 2 * t4) = make_float2(o[n][2 * q], o[n][2 * q + 1]);
-    }
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(os + (warp * kTreeDenseRows + r) * D + 8 * n + 2 * t4) =
+          make_float2(o[n][2 * q], o[n][2 * q + 1]);
   }
   __syncthreads();
-  if (!sm.odd) return;
-  for (int r = warp; r < rows; r += 4) {
-    const int i = (row0 + r) / a.G;
-    if (i >= nd) break;
-    for (int key = 0; key < nd; ++key) {
-      if (a.mask ? a.mask[b * a.m_sb + i * a.m_sn + key] == 0 : key > i) continue;
-      const __half* vs = a.dv + b * a.v_sb + key * a.v_sn + (int64_t)kvh * a.v_sh;
-      for (int c = lane; c < D; c += 32) {
-        const float v = __half2float(vs[c]);
-        if (!(fabsf(v) < INFINITY)) a.dout[(pair * a.RP + row0 + r) * D + c] += v;
-      }
+  for (int r = warp; r < kTreeDenseRows; r += 4) {
+    const int rho = row0 + r, i = rho / a.G;
+    if (rho >= a.R || i >= nd) break;
+    float top = -INFINITY, sum = 0.f, y[D / 32];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, sm.ml[k][r][0]);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = ex2_approx(sm.ml[k][r][0] - (top == -INFINITY ? 0.f : top));
+      sum = fmaf(sm.ml[k][r][1], f, sum);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) y[e] = fmaf(os[(k * kTreeDenseRows + r) * D + e * 32 + lane], f, y[e]);
     }
+    if (sm.odd)
+      for (int key = 0; key < nd; ++key) {
+        if (a.mask ? a.mask[b * a.m_sb + i * a.m_sn + key] == 0 : key > i) continue;
+        const __half* vs = a.dv + b * a.v_sb + key * a.v_sn + (int64_t)kvh * a.v_sh + lane;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+          const float v = __half2float(vs[e * 32]);
+          if (!(fabsf(v) < INFINITY)) y[e] += v;
+        }
+      }
+    const int64_t row = pair * a.RP + rho;
+    if (lane == 0) {
+      a.dm[row] = top;
+      a.dl[row] = sum;
+    }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) a.dout[row * D + e * 32 + lane] = y[e];
   }
 }
 
@@ -384,9 +356,7 @@ __global__ void __launch_bounds__(kTreeDenseThreads) tree_dense_kernel(TreeArgs 
   TreeDenseSmem<D>& sm = *reinterpret_cast<TreeDenseSmem<D>*>(smraw);
   const int64_t blk = (int64_t)blockIdx.x - 1;
   if (blk < 0) tree_partition(a);
-  else if (a.R <= 16) tree_dense<D, 4>(a, blk, sm);
-  else if (a.R <= 32) tree_dense<D, 2>(a, blk, sm);
-  else tree_dense<D, 1>(a, blk, sm);
+  else tree_dense<D>(a, blk, sm);
 }
 
 // Runs beside the dense part, which it does not read, and completes after it.
