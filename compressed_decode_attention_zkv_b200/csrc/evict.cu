@@ -3,18 +3,20 @@
 // Passages: zerokv-neo 4.0.0 (heavy_hitter_budget: a budget of tokens, the newest ones and those
 // that received the most attention).
 //
-// One thread-block cluster per (sequence, kv head).  CTA k owns a contiguous range of the tokens and
-// keeps their totals as order-preserving 32-bit keys in its shared memory (read once).
+// One thread-block cluster per (sequence, kv head); every CTA owns a contiguous range of the tokens,
+// every warp 32 KPT tokens in a row (lane = token of a group of 32), whose totals it keeps in
+// registers as order-preserving 32-bit keys: they are read once.
 //   1. The key of the last kept old token: a radix selection, 11 + 11 + 10 bits from the top.  Per
-//      pass each CTA counts the digit of its keys that match the prefix so far; the clusters' counts
-//      are summed over distributed shared memory.
+//      pass each CTA counts the digits of its keys that match the prefix so far; the cluster's
+//      counts are summed over distributed shared memory.
 //   2. A token is kept if it is among the newest, if its key is larger than that key, or if it is
-//      equal and among the first of those (lowest position).  Flags become a bit mask with counts per
-//      32 tokens, and CTA offsets.
-//   3. Destination positions, in rounds of ascending order: each thread finds the source of one
-//      destination from the bit masks, reads its codes and total, and writes them.  A source never
-//      lies before its destination, so reading a whole round before any of it is written (a cluster
-//      barrier between) makes the move safe in place.
+//      equal and among the first of those (lowest position).  A ballot makes the flags of 32 tokens
+//      a word; with g and e the larger and equal keys before a word, the kept tokens before it are
+//      g + min(e, equal keys kept), so one prefix sum gives every destination.
+//   3. Copy.  Kept neighbours go to neighbouring places.  In place, a CTA first collects its kept
+//      rows in shared memory, four bytes of each at a time, and writes after a cluster barrier: by
+//      then every source of the (sequence, kv head) has been read.
+// The cluster has as many CTAs as the range needs and, up to 8, as leave no SM without work.
 #include <cooperative_groups.h>
 
 #include "query_tables.cuh"
@@ -24,6 +26,7 @@ namespace cg = cooperative_groups;
 namespace zkv {
 
 constexpr int kEvThreads = 512;
+constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 constexpr int kEvMaxCl = 8;
 
@@ -40,7 +43,6 @@ struct EvictArgs {
   const int32_t *table, *table_out;
   int64_t max_pages, n_pages, max_pages_out, n_pages_out;
   int pshift, pshift_out;
-  int chunk;          // tokens per CTA (a multiple of 32)
   int in_place;
 };
 
@@ -53,32 +55,37 @@ __device__ __forceinline__ uint32_t total_key(float x) {
 
 struct EvictSmem {
   uint32_t hist[kEvBins];
-  uint32_t sum[kEvBins];
-  uint32_t warp[kEvThreads / 32];
+  uint32_t ws[2][kEvWarps];
   uint32_t digit, before;           // chosen digit; keys of the cluster above it
-  uint32_t cnt;                     // this CTA's count of the moment (equal keys, then kept tokens)
+  uint32_t count[2];                // this CTA's larger and equal keys
 };
 
-// exclusive prefix sum over the block; `all` = the block's total
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* ws, uint32_t& all) {
+// exclusive prefix sums of two counts over the block's warps, given each warp's totals in every lane
+__device__ __forceinline__ void warp_offsets(uint32_t x, uint32_t y, EvictSmem& sm, uint32_t& bx, uint32_t& by,
+                                             uint32_t& ax, uint32_t& ay) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t s = x;
+  if (lane == 0) {
+    sm.ws[0][warp] = x;
+    sm.ws[1][warp] = y;
+  }
+  __syncthreads();
+  bx = by = ax = ay = 0;
+#pragma unroll
+  for (int w = 0; w < kEvWarps; ++w) {
+    const uint32_t u = sm.ws[0][w], v = sm.ws[1][w];
+    if (w < warp) bx += u, by += v;
+    ax += u;
+    ay += v;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  __syncthreads();
-  if (lane == 31) ws[warp] = s;
-  __syncthreads();
-  uint32_t before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kEvThreads / 32; ++w) {
-    if (w < warp) before += ws[w];
-    all += ws[w];
-  }
-  return before + s - x;
+  return x;
 }
 
 __device__ __forceinline__ uint8_t* out_row(uint8_t* codes, const EvictArgs& a, int b, int kvh,
@@ -105,190 +112,250 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int S, const uint32_t (&
   }
 }
 
+template <int KPT>
 __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
+  constexpr int CHUNK = kEvThreads * KPT;      // tokens per CTA
   extern __shared__ __align__(16) unsigned char smraw[];
   EvictSmem& sm = *reinterpret_cast<EvictSmem*>(smraw);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smraw + sizeof(EvictSmem));   // [chunk / 32]
-  uint32_t* pre = bits + a.chunk / 32;                                       // kept before, per word
-  uint32_t* keys = pre + a.chunk / 32;                                       // [chunk]
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smraw + sizeof(EvictSmem));   // [CHUNK / 32] kept flags
+  uint32_t* pre = bits + CHUNK / 32;                                         // kept tokens of the CTA before
+  uint16_t* src = reinterpret_cast<uint16_t*>(pre + CHUNK / 32);             // [CHUNK] kept tokens
+  uint32_t* list = reinterpret_cast<uint32_t*>(src + CHUNK);                 // [CHUNK] (in place)
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t pair = blockIdx.x / C;
   const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv);
+  pdl_trigger();
   int64_t n = a.comp_len[b];
   if (n < 0 || n > a.Tcap) {
     if (tid == 0 && rank == 0) set_error(a.err, ZKV_DEVERR_COMP_LEN);
     n = n < 0 ? 0 : a.Tcap;
   }
   const bool all_kept = n <= a.keep;
-  const int64_t m = all_kept ? n : a.keep;
-  const int64_t old = all_kept ? 0 : n - a.recent;      // tokens before the newest
-  const int64_t heavy = all_kept ? 0 : a.keep - a.recent;
-  const int64_t begin = (int64_t)rank * a.chunk;
-  const int mine = (int)(n - begin < 0 ? 0 : n - begin < a.chunk ? n - begin : a.chunk);
-  const int mold = (int)(old - begin < 0 ? 0 : old - begin < a.chunk ? old - begin : a.chunk);
+  const int m = (int)(all_kept ? n : a.keep);
+  const int old = (int)(all_kept ? 0 : n - a.recent);       // tokens before the newest
+  const int heavy = (int)(all_kept ? 0 : a.keep - a.recent);
+  const int first = rank * CHUNK + warp * 32 * KPT + lane;  // this lane's tokens: first + 32 k
   const float* acc = a.acc + pair * a.Tcap;
 
   uint32_t threshold = 0u;
-  int64_t equal = 0;           // tokens with that key that are kept
+  int equal = 0;               // tokens with that key that are kept
+  uint32_t keys[KPT];
   if (heavy > 0) {
-    for (int t = tid; t < mold; t += kEvThreads) keys[t] = total_key(acc[begin + t]);
-    uint32_t prefix = 0u, mask = 0u;
-    int64_t want = heavy;      // rank of the sought key among those that match the prefix
 #pragma unroll
+    for (int k = 0; k < KPT; ++k) keys[k] = first + 32 * k < old ? total_key(acc[first + 32 * k]) : 0u;
+    uint32_t prefix = 0u, mask = 0u;
+    uint32_t want = heavy;     // rank of the sought key among those that match the prefix
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int nb = pass == 2 ? 1024 : 2048;
       for (int i = tid; i < kEvBins; i += kEvThreads) sm.hist[i] = 0u;
       __syncthreads();
-      for (int t = tid; t < mold; t += kEvThreads) {
-        const uint32_t k = keys[t];
-        if ((k & mask) == prefix) atomicAdd(&sm.hist[(k >> shift) & (nb - 1)], 1u);
-      }
+#pragma unroll
+      for (int k = 0; k < KPT; ++k)
+        if (first + 32 * k < old && (keys[k] & mask) == prefix)
+          atomicAdd(&sm.hist[(keys[k] >> shift) & (nb - 1)], 1u);
       cluster.sync();
-      // the cluster's counts; thread i sums the four highest-first digits 4 i .. 4 i + 3
-      uint32_t h[4], tot = 0;
+      // the cluster's counts from the highest digit down: thread i has digits 4 i .. 4 i + 3
+      const int d0 = nb - 4 - 4 * tid;
+      uint4 h = make_uint4(0u, 0u, 0u, 0u);    // (lowest digit first)
+      if (d0 >= 0) {
+        uint4 x[kEvMaxCl];                     // (all reads in flight)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        h[q] = 0u;
-        const int d = nb - 1 - (4 * tid + q);
-        if (d >= 0)
-          for (int c = 0; c < C; ++c) h[q] += cluster.map_shared_rank(&sm.hist[0], c)[d];
-        tot += h[q];
+        for (int c = 0; c < kEvMaxCl; ++c)
+          x[c] = c < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sm.hist[0], c) + d0)
+                       : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < kEvMaxCl; ++c) h.x += x[c].x, h.y += x[c].y, h.z += x[c].z, h.w += x[c].w;
       }
-      uint32_t all;
-      uint32_t before = block_scan(tot, sm.warp, all);
+      const uint32_t tot = h.x + h.y + h.z + h.w, incl = warp_scan(tot, lane);
+      uint32_t bx, by, ax, ay;
+      warp_offsets(__shfl_sync(0xffffffffu, incl, 31), 0u, sm, bx, by, ax, ay);
+      uint32_t before = bx + incl - tot;
+      const uint32_t hq[4] = {h.w, h.z, h.y, h.x};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (before < want && want <= (int64_t)before + h[q]) {
-          sm.digit = (uint32_t)(nb - 1 - (4 * tid + q));
+        if (before < want && want <= before + hq[q]) {
+          sm.digit = (uint32_t)(d0 + 3 - q);
           sm.before = before;
         }
-        before += h[q];
+        before += hq[q];
       }
       cluster.sync();          // (every CTA has read the counts, and this block its digit)
       prefix |= sm.digit << shift;
       mask |= (uint32_t)(nb - 1) << shift;
       want -= sm.before;
-      __syncthreads();
     }
     threshold = prefix;
-    equal = want;
+    equal = (int)want;
   }
-  // equal keys in the CTAs before this one
-  int64_t eq_before = 0;
-  const int per = (mine + kEvThreads - 1) / kEvThreads + 31;
-  const int words = (per / 32) * 1;       // 32-token words per thread, contiguous
-  const int w0 = tid * words;
-  const int nw = a.chunk / 32;
-  if (heavy > 0) {
-    uint32_t c = 0;
-    for (int w = w0; w < w0 + words && w < nw; ++w)
-      for (int i = 0; i < 32; ++i) {
-        const int t = 32 * w + ((i + lane) & 31);
-        if (t < mold && keys[t] == threshold) ++c;
-      }
-    uint32_t all;
-    const uint32_t mineq = block_scan(c, sm.warp, all);
-    if (tid == 0) sm.cnt = all;
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) eq_before += *cluster.map_shared_rank(&sm.cnt, r);
-    eq_before += mineq;
-    cluster.sync();
-  }
-  // flags and counts
-  uint32_t count = 0;
-  for (int w = w0; w < w0 + words && w < nw; ++w) {
-    uint32_t gt = 0, eq = 0, fix = 0;
-    for (int i = 0; i < 32; ++i) {
-      const int j = (i + lane) & 31, t = 32 * w + j;
-      if (t >= mine) continue;
-      if (t >= mold) {
-        fix |= 1u << j;
-      } else if (heavy > 0) {
-        if (keys[t] > threshold) gt |= 1u << j;
-        else if (keys[t] == threshold) eq |= 1u << j;
-      }
-    }
-    while (eq) {               // the lowest positions first, while there is room
-      const uint32_t low = eq & (0u - eq);
-      eq ^= low;
-      if (eq_before < equal) gt |= low;
-      ++eq_before;
-    }
-    bits[w] = gt | fix;
-    count += __popc(gt | fix);
-  }
-  uint32_t kept_here;
-  uint32_t at = block_scan(count, sm.warp, kept_here);
-  for (int w = w0; w < w0 + words && w < nw; ++w) {
-    pre[w] = at;
-    at += __popc(bits[w]);
-  }
-  // words behind the last token (no thread's share)
-  for (int w = kEvThreads * words + tid; w < nw; w += kEvThreads) {
-    bits[w] = 0u;
-    pre[w] = kept_here;
-  }
-  if (tid == 0) sm.cnt = kept_here;
-  cluster.sync();
-  uint32_t off[kEvMaxCl + 1];
-  off[0] = 0;
+  // flags: group k of the warp is word warp * KPT + k; its kept-for-certain and equal tokens
+  uint32_t gt_of = 0u, eq_of = 0u, gt_of2 = 0u, eq_of2 = 0u;     // words lane and lane + 32 of the warp
 #pragma unroll
-  for (int r = 0; r < kEvMaxCl; ++r)
-    off[r + 1] = off[r] + (r < C ? *cluster.map_shared_rank(&sm.cnt, r) : 0u);
+  for (int k = 0; k < KPT; ++k) {
+    const int t = first + 32 * k;
+    const bool is_old = t < old;
+    const unsigned gt = __ballot_sync(0xffffffffu, t < n && (!is_old || (heavy > 0 && keys[k] > threshold)));
+    const unsigned eq = __ballot_sync(0xffffffffu, is_old && heavy > 0 && keys[k] == threshold);
+    if (lane == (k & 31)) {
+      if (k < 32) gt_of = gt, eq_of = eq;
+      else gt_of2 = gt, eq_of2 = eq;
+    }
+  }
+  // (gt, eq) before each word: of the warp, the CTA and the cluster
+  uint32_t g0 = warp_scan(__popc(gt_of), lane), e0 = warp_scan(__popc(eq_of), lane);
+  uint32_t g1 = warp_scan(__popc(gt_of2), lane), e1 = warp_scan(__popc(eq_of2), lane);
+  g1 += __shfl_sync(0xffffffffu, g0, 31);
+  e1 += __shfl_sync(0xffffffffu, e0, 31);
+  uint32_t bg, be, ag, ae;
+  warp_offsets(__shfl_sync(0xffffffffu, g1, 31), __shfl_sync(0xffffffffu, e1, 31), sm, bg, be, ag, ae);
+  if (tid == 0) {
+    sm.count[0] = ag;
+    sm.count[1] = ae;
+  }
+  cluster.sync();
+  uint32_t cg0 = 0, ce0 = 0;   // of the CTAs before this one
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t* c = cluster.map_shared_rank(&sm.count[0], r);
+    cg0 += c[0];
+    ce0 += c[1];
+  }
+  auto kept_eq = [&](uint32_t e) { return e < (uint32_t)equal ? e : (uint32_t)equal; };
+  const uint32_t base = cg0 + kept_eq(ce0);            // first destination of the CTA
+  const uint32_t kept_here = cg0 + ag + kept_eq(ce0 + ae) - base;
+#pragma unroll
+  for (int q = 0; q < (KPT > 32 ? 2 : 1); ++q) {
+    const uint32_t gt = q ? gt_of2 : gt_of, eq = q ? eq_of2 : eq_of;
+    const uint32_t gb = cg0 + bg + (q ? g1 : g0) - __popc(gt);
+    const uint32_t eb = ce0 + be + (q ? e1 : e0) - __popc(eq);
+    // the lowest equal positions, while there is room
+    uint32_t take = eb < (uint32_t)equal ? (uint32_t)equal - eb : 0u, word = gt;
+    if (take >= (uint32_t)__popc(eq)) {
+      word |= eq;
+    } else {
+      for (uint32_t x = eq; take > 0u; --take, x &= x - 1u) word |= x & (0u - x);
+    }
+    if (lane + 32 * q < KPT) {
+      bits[warp * KPT + lane + 32 * q] = word;
+      pre[warp * KPT + lane + 32 * q] = gb + kept_eq(eb) - base;
+    }
+  }
+  __syncwarp();                // a warp reads its own words only
+#pragma unroll 4
+  for (int k = 0; k < KPT; ++k) {
+    const uint32_t word = bits[warp * KPT + k];
+    if (word >> lane & 1u)
+      src[pre[warp * KPT + k] + __popc(word & ((1u << lane) - 1u))] = (uint16_t)(warp * 32 * KPT + 32 * k + lane);
+  }
+  __syncthreads();
 
   const CodeRows kr = code_rows(a.k_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh, a.Hkv,
                                 a.Tcap, a.Sk, a.err);
   const CodeRows vr = code_rows(a.v_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh, a.Hkv,
                                 a.Tcap, a.Sv, a.err);
   float* acc_out = a.acc_out + pair * a.Tout;
-  const int64_t round = (int64_t)C * kEvThreads;
-  for (int64_t j0 = 0; j0 < m; j0 += round) {
-    const int64_t j = j0 + rank * kEvThreads + tid;
-    uint32_t wk[2] = {0u, 0u}, wv[2] = {0u, 0u};
-    float x = 0.f;
-    int64_t src = -1;
-    if (j < m) {
-      int r = 0;
+  const uint32_t begin = (uint32_t)rank * CHUNK;
+  // four kept tokens of this thread at a time, their reads in flight together: get(token), put(index
+  // among the CTA's kept tokens, what get gave)
+  auto each = [&](auto get, auto put) {
+    for (uint32_t i0 = tid; i0 < kept_here; i0 += 4 * kEvThreads) {
+      uint32_t t[4];
+      decltype(get(0u)) x[4];
 #pragma unroll
-      for (int q = 1; q < kEvMaxCl; ++q)
-        if (q < C && j >= off[q]) r = q;
-      const uint32_t local = (uint32_t)(j - off[r]);
-      const uint32_t* rp = cluster.map_shared_rank(pre, r);
-      const uint32_t* rb = cluster.map_shared_rank(bits, r);
-      int lo = 0, hi = nw;     // the last word with pre <= local
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (rp[mid] <= local) lo = mid;
-        else hi = mid;
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t i = i0 + u * kEvThreads;
+        t[u] = begin + src[i < kept_here ? i : i0];
       }
-      src = (int64_t)r * a.chunk + 32 * lo + __fns(rb[lo], 0, (int)(local - rp[lo]) + 1);
-      load_codes<8, false>(kr, (uint32_t)src, a.Sk, wk);
-      load_codes<8, false>(vr, (uint32_t)src, a.Sv, wv);
-      x = acc[src];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = get(t[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kEvThreads < kept_here) put(i0 + u * kEvThreads, x[u]);
     }
-    if (a.in_place) cluster.sync();
-    if (j < m) {
-      store_codes(out_row(a.k_out, a, b, kvh, j, a.Sk), a.Sk, wk);
-      store_codes(out_row(a.v_out, a, b, kvh, j, a.Sv), a.Sv, wv);
-      acc_out[j] = x;
-      if (a.kept) a.kept[pair * a.keep + j] = (int32_t)src;
+  };
+  auto total = [&](uint32_t t) { return acc[t]; };
+  if (!a.in_place) {
+    auto move = [&](const CodeRows& rows, uint8_t* out, int S) {
+      auto words = [&](auto word) {            // contiguous rows of one machine word each
+        using W = decltype(word);
+        const W* from = reinterpret_cast<const W*>(rows.base);
+        W* to = reinterpret_cast<W*>(out + ((int64_t)pair * a.Tout + base) * S);
+        each([&](uint32_t t) { return from[t]; }, [&](uint32_t i, W x) { to[i] = x; });
+      };
+      const bool plain = !a.table && !a.table_out;
+      if (plain && S == 4) return words(uint32_t());
+      if (plain && S == 2) return words(uint16_t());
+      if (plain && S == 1) return words(uint8_t());
+      if (plain && S == 8) return words(uint2());
+      each([&](uint32_t t) {
+             uint32_t w[2];
+             load_codes<8, false>(rows, t, S, w);
+             return make_uint2(w[0], w[1]);
+           },
+           [&](uint32_t i, uint2 x) {
+             const uint32_t w[2] = {x.x, x.y};
+             store_codes(out_row(out, a, b, kvh, base + i, S), S, w);
+           });
+    };
+    move(kr, a.k_out, a.Sk);
+    move(vr, a.v_out, a.Sv);
+    each(total, [&](uint32_t i, float x) { acc_out[base + i] = x; });
+  } else {
+    // four bytes of every kept row at a time: K, V (two turns each for more than four stages), totals
+    const int tk = (a.Sk + 3) / 4, tv = (a.Sv + 3) / 4;
+    for (int turn = 0; turn <= tk + tv; ++turn) {
+      const bool is_k = turn < tk, is_acc = turn == tk + tv;
+      const int part = is_k ? turn : turn - tk, S = is_k ? a.Sk : a.Sv;
+      if (is_acc) {
+        each(total, [&](uint32_t i, float x) { list[i] = __float_as_uint(x); });
+      } else if (!a.table && S == 4) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>((is_k ? kr : vr).base);
+        each([&](uint32_t t) { return from[t]; }, [&](uint32_t i, uint32_t x) { list[i] = x; });
+      } else {
+        each([&](uint32_t t) {
+               uint32_t w[2];
+               load_codes<8, false>(is_k ? kr : vr, t, S, w);
+               return part == 0 ? w[0] : w[1];
+             },
+             [&](uint32_t i, uint32_t x) { list[i] = x; });
+      }
+      cluster.sync();          // every source of this turn has been read
+      for (uint32_t i = tid; i < kept_here; i += kEvThreads) {
+        const int64_t j = base + i;
+        const uint32_t w = list[i];
+        if (is_acc) {
+          acc_out[j] = __uint_as_float(w);
+          continue;
+        }
+        uint8_t* p = out_row(is_k ? a.k_out : a.v_out, a, b, kvh, j, S);
+        if (!p) continue;
+        p += 4 * part;
+        if (S % 4 == 0) {
+          *reinterpret_cast<uint32_t*>(p) = w;
+        } else {
+          for (int s = 0; s < 4 && 4 * part + s < S; ++s) p[s] = (uint8_t)(w >> (8 * s));
+        }
+      }
+      __syncthreads();         // the list has been written out
     }
-    if (a.in_place) cluster.sync();
   }
-  // tokens to come start without a total
-  const int64_t zero_to = n < a.Tout ? n : a.Tout;
-  for (int64_t j = m + rank * kEvThreads + tid; j < zero_to; j += round) acc_out[j] = 0.f;
   if (a.kept)
-    for (int64_t j = m + rank * kEvThreads + tid; j < a.keep; j += round) a.kept[pair * a.keep + j] = -1;
+    for (uint32_t i = tid; i < kept_here; i += kEvThreads) a.kept[pair * a.keep + base + i] = (int32_t)(begin + src[i]);
+  // tokens to come start without a total (a source that another CTA has read by now: in place the
+  // totals went last, and all of them were read before the barrier)
+  const int64_t zero_to = n < a.Tout ? n : a.Tout, all = (int64_t)C * kEvThreads;
+  for (int64_t j = m + rank * kEvThreads + tid; j < zero_to; j += all) acc_out[j] = 0.f;
+  if (a.kept)
+    for (int64_t j = m + rank * kEvThreads + tid; j < a.keep; j += all) a.kept[pair * a.keep + j] = -1;
   cluster.sync();              // no CTA leaves while another may read its shared memory
 }
 
 // after every CTA has read comp_len (len_out may be the same array)
 __global__ void evict_lengths_kernel(int B, int64_t Tcap, int64_t keep, const int32_t* comp_len,
                                      int32_t* len_out) {
+  pdl_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
   int64_t n = comp_len[b];
@@ -296,7 +363,27 @@ __global__ void evict_lengths_kernel(int B, int64_t Tcap, int64_t keep, const in
   len_out[b] = (int32_t)(n < keep ? n : keep);
 }
 
-static size_t evict_smem(int chunk) { return sizeof(EvictSmem) + (size_t)chunk / 32 * 8 + (size_t)chunk * 4; }
+template <int KPT>
+static cudaError_t launch_evict(const EvictArgs& a, int C, cudaStream_t st) {
+  constexpr int CHUNK = kEvThreads * KPT;
+  constexpr size_t apart = sizeof(EvictSmem) + CHUNK / 32 * 8 + CHUNK * 2, in_place = apart + CHUNK * 4;
+  static_assert(in_place <= 227 * 1024, "fits");
+  const cudaError_t e = ensure_smem_limit(evict_kernel<KPT>, in_place);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.Hkv * C));
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = a.in_place ? in_place : apart;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<KPT>, a);
+}
 
 }  // namespace zkv
 
@@ -336,27 +423,21 @@ extern "C" int zkv_rvq_evict(const zkv_evict_params* p, void* stream) {
   a.pshift = p->block_table ? log2_pow2(p->page_tokens) : 0;
   a.pshift_out = p->block_table_out ? log2_pow2(p->page_tokens_out) : 0;
   a.in_place = codes_in_place || p->acc_out == p->acc;
+  // CTAs per cluster: what the capacity needs at 32768 tokens each, then more while there are SMs for
+  // them and each keeps 4096 tokens
+  const int64_t pairs = (int64_t)p->B * p->Hkv;
   int C = 1;
-  while (C < kEvMaxCl && p->Tcap > (int64_t)C * 4096) C *= 2;
+  while (p->Tcap > (int64_t)C * kEvThreads * 64) C *= 2;
+  while (C < kEvMaxCl && pairs * C * 2 <= 148 && p->Tcap > (int64_t)C * 4096) C *= 2;
   const int64_t per = (p->Tcap + C - 1) / C;
-  a.chunk = (int)((per + 31) / 32 * 32);
-  const size_t smem = evict_smem(a.chunk);
-  if (ensure_smem_limit(evict_kernel, smem) != cudaSuccess) return ZKV_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p->B * p->Hkv * C));
-  cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_kernel, a) != cudaSuccess) return ZKV_ERR_CUDA;
-  evict_lengths_kernel<<<(p->B + 127) / 128, 128, 0, st>>>(p->B, p->Tcap, p->keep, p->comp_len, p->len_out);
-  ZKV_CHECK_LAUNCH();
+  const cudaError_t e = per <= kEvThreads * 2    ? launch_evict<2>(a, C, st)
+                        : per <= kEvThreads * 8  ? launch_evict<8>(a, C, st)
+                        : per <= kEvThreads * 32 ? launch_evict<32>(a, C, st)
+                                                 : launch_evict<64>(a, C, st);
+  if (e != cudaSuccess) return ZKV_ERR_CUDA;
+  if (launch_pdl(evict_lengths_kernel, dim3((p->B + 127) / 128), dim3(128), 0, st, (int)p->B, p->Tcap, p->keep,
+                 p->comp_len, p->len_out) != cudaSuccess)
+    return ZKV_ERR_CUDA;
   return ZKV_OK;
 }

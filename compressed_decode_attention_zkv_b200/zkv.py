@@ -35,7 +35,7 @@ ZKV_DEVERR_DRAFT = 32
 ZKV_DTYPE_F16, ZKV_DTYPE_F32 = 0, 1
 CODEBOOK_SIZE = 256
 DECODE_SCRATCH_BYTES = 8 << 20   # ZKV_DECODE_SCRATCH_BYTES: the no-allocation decode's array
-EVICT_MAX_TOKENS = 393216        # ZKV_EVICT_MAX_TOKENS: the largest capacity that rvq_evict takes
+EVICT_MAX_TOKENS = 262144        # ZKV_EVICT_MAX_TOKENS: the largest capacity that rvq_evict takes
 
 
 class ZkvError(RuntimeError):

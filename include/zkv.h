@@ -665,7 +665,7 @@ int zkv_rvq_accumulate_weights(const zkv_weights_params* p, void* workspace,
  * source reads as code 0, a row of a bad destination page is not written (ZKV_DEVERR_PAGE).
  * No workspace.  Errors: INVALID_ARG, UNSUPPORTED (S, Tcap > ZKV_EVICT_MAX_TOKENS), CUDA.
  */
-#define ZKV_EVICT_MAX_TOKENS 393216
+#define ZKV_EVICT_MAX_TOKENS 262144
 typedef struct {
   int B, Hkv, Sk, Sv;
   int64_t Tcap, Tcap_out, keep, recent;

@@ -231,6 +231,8 @@ EVICT = {
     "all but one": dict(case=dict(B=1, Hkv=1, Sk=7, Sv=6, Tcap=9000, comp=[8999]), keep=8998, recent=1),
     "a cluster of 8": dict(case=dict(B=1, Hkv=2, Sk=4, Sv=4, Tcap=40000, comp=[39999]), keep=10001, recent=256),
     "few in a large one": dict(case=dict(B=2, Hkv=1, Sk=4, Sv=4, Tcap=40000, comp=[600, 31000]), keep=500, recent=3),
+    "the largest": dict(case=dict(B=1, Hkv=1, Sk=1, Sv=6, Tcap=262144, comp=[262143]), keep=100001, recent=500),
+    "the largest, ties": dict(case=dict(B=1, Hkv=1, Sk=8, Sv=1, Tcap=262144, comp=[200000], ties=True), keep=150000, recent=0),
     "ties over ctas": dict(case=dict(B=1, Hkv=1, Sk=2, Sv=2, Tcap=30000, comp=[30000], ties=True), keep=20000, recent=7),
 }
 
