@@ -25,7 +25,7 @@ namespace cg = cooperative_groups;
 
 namespace zkv {
 
-constexpr int kEvThreads = 512;
+constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 constexpr int kEvMaxCl = 8;
@@ -57,28 +57,9 @@ struct EvictSmem {
   uint32_t hist[kEvBins];
   uint32_t ws[2][kEvWarps];
   uint32_t digit, before;           // chosen digit; keys of the cluster above it
-  uint32_t count[2];                // this CTA's larger and equal keys
+  alignas(8) uint32_t count[2];     // this CTA's larger and equal keys
 };
 
-// exclusive prefix sums of two counts over the block's warps, given each warp's totals in every lane
-__device__ __forceinline__ void warp_offsets(uint32_t x, uint32_t y, EvictSmem& sm, uint32_t& bx, uint32_t& by,
-                                             uint32_t& ax, uint32_t& ay) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) {
-    sm.ws[0][warp] = x;
-    sm.ws[1][warp] = y;
-  }
-  __syncthreads();
-  bx = by = ax = ay = 0;
-#pragma unroll
-  for (int w = 0; w < kEvWarps; ++w) {
-    const uint32_t u = sm.ws[0][w], v = sm.ws[1][w];
-    if (w < warp) bx += u, by += v;
-    ax += u;
-    ay += v;
-  }
-  __syncthreads();
-}
 __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {   // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -88,6 +69,24 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x, int lane) {   // inclu
   return x;
 }
 
+// exclusive prefix sums of two counts over the block's warps, given each warp's totals in every lane
+__device__ __forceinline__ void warp_offsets(uint32_t x, uint32_t y, EvictSmem& sm, uint32_t& bx, uint32_t& by,
+                                             uint32_t& ax, uint32_t& ay) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  static_assert(kEvWarps == 32, "one lane per warp");
+  if (lane == 0) {
+    sm.ws[0][warp] = x;
+    sm.ws[1][warp] = y;
+  }
+  __syncthreads();
+  const uint32_t u = sm.ws[0][lane], v = sm.ws[1][lane];
+  const uint32_t su = warp_scan(u, lane), sv = warp_scan(v, lane);
+  bx = __shfl_sync(0xffffffffu, su - u, warp);
+  by = __shfl_sync(0xffffffffu, sv - v, warp);
+  ax = __shfl_sync(0xffffffffu, su, 31);
+  ay = __shfl_sync(0xffffffffu, sv, 31);
+  __syncthreads();
+}
 __device__ __forceinline__ uint8_t* out_row(uint8_t* codes, const EvictArgs& a, int b, int kvh,
                                             int64_t t, int S) {
   if (!a.table_out) return codes + (((int64_t)b * a.Hkv + kvh) * a.Tout + t) * S;
@@ -158,30 +157,27 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
         if (first + 32 * k < old && (keys[k] & mask) == prefix)
           atomicAdd(&sm.hist[(keys[k] >> shift) & (nb - 1)], 1u);
       cluster.sync();
-      // the cluster's counts from the highest digit down: thread i has digits 4 i .. 4 i + 3
-      const int d0 = nb - 4 - 4 * tid;
-      uint4 h = make_uint4(0u, 0u, 0u, 0u);    // (lowest digit first)
+      // the cluster's counts from the highest digit down: thread i has digits 2 i and 2 i + 1
+      static_assert(kEvBins == 2 * kEvThreads, "two digits per thread");
+      const int d0 = nb - 2 - 2 * tid;
+      uint2 h = make_uint2(0u, 0u);            // (lower digit first)
       if (d0 >= 0) {
-        uint4 x[kEvMaxCl];                     // (all reads in flight)
+        uint2 x[kEvMaxCl];                     // (all reads in flight)
 #pragma unroll
         for (int c = 0; c < kEvMaxCl; ++c)
-          x[c] = c < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sm.hist[0], c) + d0)
-                       : make_uint4(0u, 0u, 0u, 0u);
+          x[c] = c < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[0], c) + d0)
+                       : make_uint2(0u, 0u);
 #pragma unroll
-        for (int c = 0; c < kEvMaxCl; ++c) h.x += x[c].x, h.y += x[c].y, h.z += x[c].z, h.w += x[c].w;
+        for (int c = 0; c < kEvMaxCl; ++c) h.x += x[c].x, h.y += x[c].y;
       }
-      const uint32_t tot = h.x + h.y + h.z + h.w, incl = warp_scan(tot, lane);
+      const uint32_t tot = h.x + h.y, incl = warp_scan(tot, lane);
       uint32_t bx, by, ax, ay;
       warp_offsets(__shfl_sync(0xffffffffu, incl, 31), 0u, sm, bx, by, ax, ay);
-      uint32_t before = bx + incl - tot;
-      const uint32_t hq[4] = {h.w, h.z, h.y, h.x};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (before < want && want <= before + hq[q]) {
-          sm.digit = (uint32_t)(d0 + 3 - q);
-          sm.before = before;
-        }
-        before += hq[q];
+      const uint32_t before = bx + incl - tot;
+      if (before < want && want <= before + tot) {
+        const bool upper = want <= before + h.y;
+        sm.digit = (uint32_t)(d0 + (upper ? 1 : 0));
+        sm.before = before + (upper ? 0u : h.y);
       }
       cluster.sync();          // (every CTA has read the counts, and this block its digit)
       prefix |= sm.digit << shift;
@@ -192,55 +188,47 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
     equal = (int)want;
   }
   // flags: group k of the warp is word warp * KPT + k; its kept-for-certain and equal tokens
-  uint32_t gt_of = 0u, eq_of = 0u, gt_of2 = 0u, eq_of2 = 0u;     // words lane and lane + 32 of the warp
+  static_assert(KPT <= 32, "one lane per word");
+  uint32_t gt_of = 0u, eq_of = 0u;                          // word lane of the warp
 #pragma unroll
   for (int k = 0; k < KPT; ++k) {
     const int t = first + 32 * k;
     const bool is_old = t < old;
     const unsigned gt = __ballot_sync(0xffffffffu, t < n && (!is_old || (heavy > 0 && keys[k] > threshold)));
     const unsigned eq = __ballot_sync(0xffffffffu, is_old && heavy > 0 && keys[k] == threshold);
-    if (lane == (k & 31)) {
-      if (k < 32) gt_of = gt, eq_of = eq;
-      else gt_of2 = gt, eq_of2 = eq;
-    }
+    if (lane == k) gt_of = gt, eq_of = eq;
   }
   // (gt, eq) before each word: of the warp, the CTA and the cluster
-  uint32_t g0 = warp_scan(__popc(gt_of), lane), e0 = warp_scan(__popc(eq_of), lane);
-  uint32_t g1 = warp_scan(__popc(gt_of2), lane), e1 = warp_scan(__popc(eq_of2), lane);
-  g1 += __shfl_sync(0xffffffffu, g0, 31);
-  e1 += __shfl_sync(0xffffffffu, e0, 31);
+  const uint32_t g = warp_scan(__popc(gt_of), lane), e = warp_scan(__popc(eq_of), lane);
   uint32_t bg, be, ag, ae;
-  warp_offsets(__shfl_sync(0xffffffffu, g1, 31), __shfl_sync(0xffffffffu, e1, 31), sm, bg, be, ag, ae);
+  warp_offsets(__shfl_sync(0xffffffffu, g, 31), __shfl_sync(0xffffffffu, e, 31), sm, bg, be, ag, ae);
   if (tid == 0) {
     sm.count[0] = ag;
     sm.count[1] = ae;
   }
   cluster.sync();
   uint32_t cg0 = 0, ce0 = 0;   // of the CTAs before this one
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* c = cluster.map_shared_rank(&sm.count[0], r);
-    cg0 += c[0];
-    ce0 += c[1];
-  }
+#pragma unroll
+  for (int r = 0; r < kEvMaxCl - 1; ++r)
+    if (r < rank) {
+      const uint2 c = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.count[0], r));
+      cg0 += c.x;
+      ce0 += c.y;
+    }
   auto kept_eq = [&](uint32_t e) { return e < (uint32_t)equal ? e : (uint32_t)equal; };
   const uint32_t base = cg0 + kept_eq(ce0);            // first destination of the CTA
   const uint32_t kept_here = cg0 + ag + kept_eq(ce0 + ae) - base;
-#pragma unroll
-  for (int q = 0; q < (KPT > 32 ? 2 : 1); ++q) {
-    const uint32_t gt = q ? gt_of2 : gt_of, eq = q ? eq_of2 : eq_of;
-    const uint32_t gb = cg0 + bg + (q ? g1 : g0) - __popc(gt);
-    const uint32_t eb = ce0 + be + (q ? e1 : e0) - __popc(eq);
+  if (lane < KPT) {
+    const uint32_t gb = cg0 + bg + g - __popc(gt_of), eb = ce0 + be + e - __popc(eq_of);
     // the lowest equal positions, while there is room
-    uint32_t take = eb < (uint32_t)equal ? (uint32_t)equal - eb : 0u, word = gt;
-    if (take >= (uint32_t)__popc(eq)) {
-      word |= eq;
+    uint32_t take = eb < (uint32_t)equal ? (uint32_t)equal - eb : 0u, word = gt_of;
+    if (take >= (uint32_t)__popc(eq_of)) {
+      word |= eq_of;
     } else {
-      for (uint32_t x = eq; take > 0u; --take, x &= x - 1u) word |= x & (0u - x);
+      for (uint32_t x = eq_of; take > 0u; --take, x &= x - 1u) word |= x & (0u - x);
     }
-    if (lane + 32 * q < KPT) {
-      bits[warp * KPT + lane + 32 * q] = word;
-      pre[warp * KPT + lane + 32 * q] = gb + kept_eq(eb) - base;
-    }
+    bits[warp * KPT + lane] = word;
+    pre[warp * KPT + lane] = gb + kept_eq(eb) - base;
   }
   __syncwarp();                // a warp reads its own words only
 #pragma unroll 4
@@ -427,14 +415,14 @@ extern "C" int zkv_rvq_evict(const zkv_evict_params* p, void* stream) {
   // them and each keeps 4096 tokens
   const int64_t pairs = (int64_t)p->B * p->Hkv;
   int C = 1;
-  while (p->Tcap > (int64_t)C * kEvThreads * 64) C *= 2;
+  while (p->Tcap > (int64_t)C * kEvThreads * 32) C *= 2;
   while (C < kEvMaxCl && pairs * C * 2 <= 148 && p->Tcap > (int64_t)C * 4096) C *= 2;
   const int64_t per = (p->Tcap + C - 1) / C;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = per <= kEvThreads * 2    ? launch_evict<2>(a, C, st)
-                        : per <= kEvThreads * 8  ? launch_evict<8>(a, C, st)
-                        : per <= kEvThreads * 32 ? launch_evict<32>(a, C, st)
-                                                 : launch_evict<64>(a, C, st);
+  const cudaError_t e = per <= kEvThreads        ? launch_evict<1>(a, C, st)
+                        : per <= kEvThreads * 4  ? launch_evict<4>(a, C, st)
+                        : per <= kEvThreads * 16 ? launch_evict<16>(a, C, st)
+                                                 : launch_evict<32>(a, C, st);
   if (e != cudaSuccess) return ZKV_ERR_CUDA;
   if (launch_pdl(evict_lengths_kernel, dim3((p->B + 127) / 128), dim3(128), 0, st, (int)p->B, p->Tcap, p->keep,
                  p->comp_len, p->len_out) != cudaSuccess)
