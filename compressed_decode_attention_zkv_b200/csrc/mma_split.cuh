@@ -63,6 +63,11 @@ template <int K>
 __device__ __forceinline__ void frag_b(uint32_t (&b)[4], const __half* t, int n0, int ks, int lane) {
   ldsm4(b, t + tile_at<K>(n0 + (lane & 7) + ((lane >> 4) << 3), ks * 16 + 8 * ((lane >> 3) & 1)));
 }
+// B of 8 columns for two steps, ks and ks + 1 (b[0], b[1]: ks; b[2], b[3]: ks + 1)
+template <int K>
+__device__ __forceinline__ void frag_b2(uint32_t (&b)[4], const __half* t, int n0, int ks, int lane) {
+  ldsm4(b, t + tile_at<K>(n0 + (lane & 7), ks * 16 + 8 * (lane >> 3)));
+}
 // The same from tiles that hold the sum's index as rows: A^T [k][M], B [k][N]
 template <int M>
 __device__ __forceinline__ void frag_at(uint32_t (&a)[4], const __half* t, int r0, int ks, int lane) {

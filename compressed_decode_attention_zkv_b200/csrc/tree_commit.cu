@@ -11,18 +11,29 @@
 // token of that slot if there was one, else the window's own token.
 //
 // Kernel 1: the evictions of all sequences are numbered through (a prefix sum that every block
-// computes for itself), so a cluster of 8 CTAs (append_cluster.cuh) encodes eight evictions of one
-// kv head and of K or V, from whichever sequences.  Only the first eviction of a slot (k < W) reads
-// the window, and its cluster then writes the slot's last token; fill slots that no eviction takes
-// are written apart.  So no slot is read by one cluster and written by another.
+// computes for itself), so a block encodes R evictions of one kv head and of K or V, from whichever
+// sequences.  R is 16 (one warp each); where that could make more blocks than SMs it is 32, since a
+// block's time is mostly that of the codewords it reads and splits.  Only the first eviction of a slot (k < W) reads the window, and its block then writes
+// the slot's last token; fill slots that no eviction takes are written apart.  So no slot is read by
+// one block and written by another.
 // Kernel 2 advances the lengths after all of kernel 1 has read them.
-#include "append_cluster.cuh"
-
+//
+// Encode.  Per stage the distances ||c||^2 - 2 r . c of the R residuals to all 256 codewords come
+// from the tensor cores (mma_split.cuh), in chunks of CH codewords whose loads are in flight during
+// the chunk before.  Their error is below the row encoder's margin for float32 sums (candidate_margin
+// allows 2.5 d 2^-24 (||r|| + ||c||)^2; the split product is off by less than 2^-21 ||r|| ||c|| and
+// ||c||^2 by d 2^-24 of itself), so the codewords within that margin of the smallest distance hold
+// the nearest one: if there is one it is the choice, else the distances are taken again in float64
+// and ties go to the lowest index, as zkv_rvq_encode decides.
+#include <cfloat>
 #include <cmath>
 
-namespace cg = cooperative_groups;
+#include "encode_rows.cuh"
+#include "mma_split.cuh"
 
 namespace zkv {
+
+constexpr int kCommitThreads = 512;
 
 struct CommitState {
   int64_t n, wl, head, comp, evict, fill;   // fill: tokens that take free slots
@@ -41,9 +52,13 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
     err = ZKV_DEVERR_DRAFT;
     return false;
   }
-  for (int64_t i = 0; i < s.n; ++i) {
-    const int32_t x = p.path[b * p.M + i];
-    if (x < 0 || x >= p.N) err = ZKV_DEVERR_DRAFT;
+  for (int64_t i = 0; i < s.n; i += 8) {
+    int32_t x[8];                    // (eight loads in flight)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = i + q < s.n ? p.path[b * p.M + i + q] : 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (x[q] < 0 || x[q] >= p.N) err = ZKV_DEVERR_DRAFT;
   }
   if (err) return false;
   if (s.wl < 0 || s.wl > p.Wcap) {
@@ -71,23 +86,43 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
   return s.n > 0;
 }
 
-template <int D>
-__global__ void __cluster_dims__(kAppendCl, 1, 1) __launch_bounds__(256)
-    tree_commit_kernel(zkv_tree_commit_params p, double rot) {
+template <int D, int R>
+struct CommitSmem {
+  static constexpr int CH = D == 256 ? 64 : 128;      // codewords per chunk
+  __half c[2][CH * D];                                // codewords, high and low plane
+  __half x[2][R * D];                       // residuals
+  float r[R][D + 4];                        // residuals, float32
+  float dist[R][kCodebook + 4];
+  float cn[kCodebook];                                // squared norms of the stage's codewords
+  float cs[CH];                                       // scales of the chunk's codewords
+  float xs[R];                              // scales of the residuals
+  double rn[R];                             // bound of their norms
+  uint8_t code[R][kMaxStages];
+  int row_b[R];                             // the evictions: sequence (-1: none), k, state
+  int64_t row_k[R];
+  CommitState row_s[R];
+  int64_t warp_sum[kCommitThreads / 32];
+};
+
+// a lane that TransposeSum<N, N, 16> leaves the sum of value k with
+template <int N>
+__device__ __forceinline__ constexpr int owner(int k) {
+  int lane = 0;
+  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2)
+    if (k & n) lane |= o;
+  return lane;
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_commit_params p, double rot) {
+  constexpr int E = D / 32, CH = CommitSmem<D, R>::CH, NC = kCodebook / CH, CW = CH / 16;   // CW: codewords per warp
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  AppendSmem<D>& sm = *reinterpret_cast<AppendSmem<D>*>(smem_raw);
-  __shared__ int64_t warp_sum[8];
-  __shared__ int row_b[kAppendR];                 // the cluster's evictions: sequence (-1: none), k
-  __shared__ int64_t row_k[kAppendR];
-  __shared__ CommitState row_s[kAppendR];
+  CommitSmem<D, R>& sm = *reinterpret_cast<CommitSmem<D, R>*>(smem_raw);
   pdl_trigger();   // the length update may launch now; it waits for this kernel's completion
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kind = blockIdx.z;   // 0 = keys, 1 = values
   const int h = blockIdx.y;
-  const int64_t group = blockIdx.x / kAppendCl, groups = gridDim.x / kAppendCl;
-  const int64_t row0 = group * kAppendR;
+  const int64_t row0 = (int64_t)blockIdx.x * R;
   const int S = kind ? p.Sv : p.Sk;
   const float* CB = (kind ? p.v_codebooks : p.k_codebooks) + (size_t)h * S * kCodebook * D;
   __half* win = reinterpret_cast<__half*>(kind ? p.win_v : p.win_k);
@@ -98,9 +133,28 @@ __global__ void __cluster_dims__(kAppendCl, 1, 1) __launch_bounds__(256)
   auto token = [&](int64_t b, int64_t i) -> const __half* {     // accepted token i of sequence b
     return draft + b * sb + (int64_t)p.path[b * p.M + i] * sn + (int64_t)h * sh;
   };
-  if (tid < kAppendR) row_b[tid] = -1;
+  // codewords of a chunk: warp w holds CW w .. CW w + CW - 1, lane = E dimensions in a row
+  float cw[CW][E];
+  auto load = [&](int q) {       // chunk q of all stages' chunks
+    const float* C = CB + ((size_t)q * CH + CW * warp) * D + lane * E;
+#pragma unroll
+    for (int k = 0; k < CW; ++k) {
+      if constexpr (E == 2) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(C + k * D));
+        cw[k][0] = v.x; cw[k][1] = v.y;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(C + k * D + e));
+          cw[k][e] = v.x; cw[k][e + 1] = v.y; cw[k][e + 2] = v.z; cw[k][e + 3] = v.w;
+        }
+      }
+    }
+  };
+  if (blockIdx.x == 0) load(0);  // in flight while the evictions are numbered (later blocks may have none)
+  if (tid < R) sm.row_b[tid] = -1;
   int64_t base = 0;
-  for (int64_t b0 = 0; b0 < p.B && base < row0 + kAppendR; b0 += 256) {
+  for (int64_t b0 = 0; b0 < p.B && base < row0 + R; b0 += kCommitThreads) {
     const int64_t b = b0 + tid;
     CommitState s;
     s.evict = 0;
@@ -113,40 +167,203 @@ __global__ void __cluster_dims__(kAppendCl, 1, 1) __launch_bounds__(256)
       if (lane >= o) x += y;
     }
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = x;
+    if (lane == 31) sm.warp_sum[warp] = x;
     __syncthreads();
     int64_t before = base + x - s.evict, all = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += warp_sum[w];
-      all += warp_sum[w];
+    for (int w = 0; w < kCommitThreads / 32; ++w) {
+      if (w < warp) before += sm.warp_sum[w];
+      all += sm.warp_sum[w];
     }
-    for (int r = 0; r < kAppendR; ++r) {
+    for (int r = 0; r < R; ++r) {
       const int64_t k = row0 + r - before;
       if (k >= 0 && k < s.evict) {
-        row_b[r] = (int)b;
-        row_k[r] = k;
-        row_s[r] = s;
+        sm.row_b[r] = (int)b;
+        sm.row_k[r] = k;
+        sm.row_s[r] = s;
       }
     }
     base += all;
   }
-  cluster.sync();      // (the rows are known, and every CTA of the cluster runs)
-  if (row_b[0] >= 0) {          // the same in every CTA of the cluster: rows fill from the front
-    encode_cluster<D>(
-        sm,
-        [&](int r) -> const __half* {
-          const int64_t b = row_b[r];
-          if (b < 0) return nullptr;
-          const int64_t k = row_k[r];
-          if (k >= p.Wcap) return token(b, p.Wcap - row_s[r].wl + k - p.Wcap);
-          const int64_t slot = (row_s[r].head + k) % p.Wcap;
-          if (slot >= row_s[r].wl) return token(b, slot - row_s[r].wl);
-          return win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
-        },
-        CB, S, kind == 0 && p.k_smooth ? p.k_smooth + (int64_t)h * D : nullptr, rot);
-    cluster.sync();   // no CTA leaves while another may still read its shared memory
-    if (rank == 0 && tid < kAppendR && row_b[tid] >= 0) {
-      const int64_t b = row_b[tid], t = row_s[tid].comp + row_k[tid];
+  __syncthreads();
+  if (sm.row_b[0] >= 0) {          // rows fill from the front
+    if (blockIdx.x > 0) load(0);
+    // residual row r of this warp: v (elements 32 e + lane) to shared memory, float32 and split
+    auto put_row = [&](int r, const float (&v)[E]) {
+      float ss = 0.f, big = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        ss = fmaf(v[e], v[e], ss);
+        big = fmaxf(big, fabsf(v[e]));
+      }
+      ss = warp_sum_f32(ss);
+      const int ex = split_exponent(warp_max_f32(big));
+      const float down = exp2_int(-ex);
+      if (lane == 0) {
+        sm.xs[r] = exp2_int(ex);
+        sm.rn[r] = sqrt((double)ss) * (1.0 + 1e-4);       // (D + 5 roundings of 2^-24 on ss)
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        sm.r[r][e * 32 + lane] = v[e];
+        const int at = tile_at<D>(r, e * 32 + lane);
+        split(v[e] * down, sm.x[0][at], sm.x[1][at]);
+      }
+    };
+#pragma unroll
+    for (int r = warp; r < R; r += 16) {
+      const int64_t b = sm.row_b[r];
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = 0.f;
+      if (b >= 0) {
+        const int64_t k = sm.row_k[r], slot = (sm.row_s[r].head + k) % p.Wcap, wl = sm.row_s[r].wl;
+        const __half* x = k >= p.Wcap ? token(b, k - wl)               // the token of eviction k - W
+                        : slot >= wl  ? token(b, slot - wl)            // a fill token
+                                      : win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
+        double v[E];
+        load_row_f64<E>(x, ZKV_DTYPE_F16, 0, lane, v);
+        if (kind == 0 && p.k_smooth) {   // keys: x / lambda per channel before the rotation
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] *= 1.0 / (double)p.k_smooth[(int64_t)h * D + e * 32 + lane];
+        }
+        fwht_warp_f64<D>(v, lane);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = (float)(v[e] * rot);
+      }
+      put_row(r, y);
+    }
+    const int g = lane >> 2, t4 = lane & 3;
+    for (int s = 0; s < S; ++s) {
+      for (int chunk = 0; chunk < NC; ++chunk) {
+        if (s + chunk > 0) __syncthreads();       // the previous chunk has been read
+        // their norms: lane l gets codeword l % CW's (CW sums over the lanes at once)
+        float part[CW], down_of;
+#pragma unroll
+        for (int k = 0; k < CW; ++k) {
+          part[k] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) part[k] = fmaf(cw[k][e], cw[k][e], part[k]);
+        }
+        {
+          int own = 0;
+          const float ss = TransposeSum<CW, CW, 16>::run(part, lane, own);
+          // no element is larger than the norm: scale by its power of two
+          const int ex = split_exponent(sqrtf(ss));
+          down_of = exp2_int(-ex);
+          sm.cn[chunk * CH + CW * warp + own] = ss;
+          sm.cs[CW * warp + own] = exp2_int(ex);
+        }
+#pragma unroll
+        for (int k = 0; k < CW; ++k) {
+          const int c = CW * warp + k;
+          const float down = __shfl_sync(0xffffffffu, down_of, owner<CW>(k));
+          alignas(16) __half hi[E], lo[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
+          const int at = tile_at<D>(c, lane * E);
+          if constexpr (E == 2) {
+            *reinterpret_cast<uint32_t*>(sm.c[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
+            *reinterpret_cast<uint32_t*>(sm.c[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
+          } else if constexpr (E == 4) {
+            *reinterpret_cast<uint2*>(sm.c[0] + at) = *reinterpret_cast<const uint2*>(hi);
+            *reinterpret_cast<uint2*>(sm.c[1] + at) = *reinterpret_cast<const uint2*>(lo);
+          } else {
+            *reinterpret_cast<uint4*>(sm.c[0] + at) = *reinterpret_cast<const uint4*>(hi);
+            *reinterpret_cast<uint4*>(sm.c[1] + at) = *reinterpret_cast<const uint4*>(lo);
+          }
+        }
+        __syncthreads();
+        if (s * NC + chunk + 1 < S * NC) load(s * NC + chunk + 1);
+        if (8 * warp < CH) {         // 8 codewords per warp
+          float acc[R / 16][4] = {}, cross[R / 16][2][4] = {};
+#pragma unroll 2
+          for (int ks = 0; ks < D / 16; ks += 2) {
+            uint32_t bh[4], bl[4];
+            frag_b2<D>(bh, sm.c[0], 8 * warp, ks, lane);
+            frag_b2<D>(bl, sm.c[1], 8 * warp, ks, lane);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int q = 0; q < R / 16; ++q) {
+                uint32_t ah[4], al[4];
+                frag_a<D>(ah, sm.x[0], 16 * q, ks + i, lane);
+                frag_a<D>(al, sm.x[1], 16 * q, ks + i, lane);
+                mma16816_add(acc[q], ah, bh[2 * i], bh[2 * i + 1]);
+                mma16816(cross[q][0], ah, bl[2 * i], bl[2 * i + 1]);
+                mma16816(cross[q][1], al, bh[2 * i], bh[2 * i + 1]);
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < R / 16; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 8 * warp + 2 * t4 + (i & 1), r = 16 * q + g + 8 * (i >> 1);
+              const float dot = (acc[q][i] + (cross[q][0][i] + cross[q][1][i])) * sm.cs[c] * sm.xs[r];
+              sm.dist[r][chunk * CH + c] = sm.cn[chunk * CH + c] - 2.f * dot;
+            }
+        }
+      }
+      __syncthreads();
+      // warp w decides rows w, w + 16: lane = codewords lane + 32 j
+      float cmax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax = fmaxf(cmax, sm.cn[32 * j + lane]);
+      cmax = warp_max_f32(cmax);
+#pragma unroll 1
+      for (int r = warp; r < R; r += 16) {
+        if (sm.row_b[r] < 0) break;
+        float d[8], dmin = INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          d[j] = sm.dist[r][32 * j + lane];
+          dmin = fminf(dmin, d[j]);
+        }
+        dmin = warp_min_f32(dmin);
+        const double thr = (double)dmin + candidate_margin(sm.rn[r], cmax, D);
+        unsigned cand[8];
+        int count = 0, z = kCodebook;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          cand[j] = __ballot_sync(0xffffffffu, (double)d[j] <= thr);
+          count += __popc(cand[j]);
+          if (cand[j] && z == kCodebook) z = 32 * j + __ffs(cand[j]) - 1;
+        }
+        const float* C = CB + (size_t)s * kCodebook * D;
+        if (count > 1) {           // several within the margin: float64 distances
+          double best = DBL_MAX;
+          z = kCodebook;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            for (unsigned x = cand[j]; x; x &= x - 1u) {
+              const int c = 32 * j + __ffs(x) - 1;
+              double a = 0.0;
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                const double df = (double)sm.r[r][e * 32 + lane] - (double)__ldg(C + (size_t)c * D + e * 32 + lane);
+                a = fma(df, df, a);
+              }
+              a = warp_sum_f64(a);
+              if (a < best) {      // (ascending indices: ties keep the lowest)
+                best = a;
+                z = c;
+              }
+            }
+        }
+        // a row that is not finite matches no candidate: code 0
+        if (z >= kCodebook) z = 0;
+        if (lane == 0) sm.code[r][s] = (uint8_t)z;
+        if (s + 1 < S) {
+          float v[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] = sm.r[r][e * 32 + lane] - __ldg(C + (size_t)z * D + e * 32 + lane);
+          put_row(r, v);
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < R && sm.row_b[tid] >= 0) {
+      const int64_t b = sm.row_b[tid], t = sm.row_s[tid].comp + sm.row_k[tid];
       uint8_t* c = codes + ((b * p.Hkv + h) * p.Tcap + t) * S;
       if (p.block_table) {
         const int64_t P = p.page_tokens;
@@ -154,17 +371,19 @@ __global__ void __cluster_dims__(kAppendCl, 1, 1) __launch_bounds__(256)
       }
       for (int s = 0; s < S; ++s) c[s] = sm.code[tid][s];
     }
-    // every CTA read the evicted slots before its first cluster barrier
-    if (rank == 0 && row_b[warp] >= 0 && row_k[warp] < p.Wcap) {
-      const int64_t b = row_b[warp], k = row_k[warp], e = row_s[warp].evict;
+    // (the evicted slots have been read)
+    for (int r = warp; r < R; r += 16) {
+      if (sm.row_b[r] < 0 || sm.row_k[r] >= p.Wcap) continue;
+      const int64_t b = sm.row_b[r], k = sm.row_k[r], e = sm.row_s[r].evict;
       const int64_t last = k + (e - 1 - k) / p.Wcap * p.Wcap;     // the slot's last eviction
-      const __half* src = token(b, p.Wcap - row_s[warp].wl + last);
-      __half* dst = win + ((b * p.Hkv + h) * p.Wcap + (row_s[warp].head + k) % p.Wcap) * D;
+      const __half* src = token(b, p.Wcap - sm.row_s[r].wl + last);
+      __half* dst = win + ((b * p.Hkv + h) * p.Wcap + (sm.row_s[r].head + k) % p.Wcap) * D;
       for (int i = lane; i < D; i += 32) dst[i] = src[i];
     }
   }
-  // fill tokens whose slot no eviction takes: the sequences are shared out over CTAs and warps
-  for (int64_t b = (group * kAppendCl + rank) * 8 + warp; b < p.B; b += groups * kAppendCl * 8) {
+  // fill tokens whose slot no eviction takes: the sequences are shared out over blocks and warps
+  for (int64_t b = (int64_t)blockIdx.x * 16 + warp; b < p.B; b += (int64_t)gridDim.x * 16) {
+    if (p.win_len[b] == p.Wcap) continue;      // no free slot
     CommitState s;
     int err;
     if (!commit_state(p, b, s, err)) continue;
@@ -194,18 +413,23 @@ __global__ void tree_commit_lengths_kernel(zkv_tree_commit_params p) {
   }
 }
 
-template <int D>
-static int launch_tree_commit(const zkv_tree_commit_params& p, cudaStream_t st) {
+template <int D, int R>
+static int launch_tree_commit_rows(const zkv_tree_commit_params& p, cudaStream_t st) {
   const double rot = 1.0 / std::sqrt((double)p.d);
-  if (ensure_smem_limit(tree_commit_kernel<D>, sizeof(AppendSmem<D>)) != cudaSuccess)
-    return ZKV_ERR_CUDA;
-  const int64_t groups = ((int64_t)p.B * p.M + kAppendR - 1) / kAppendR;
-  const dim3 grid((unsigned)(groups * kAppendCl), (unsigned)p.Hkv, 2);
-  tree_commit_kernel<D><<<grid, 256, sizeof(AppendSmem<D>), st>>>(p, rot);
+  static_assert(sizeof(CommitSmem<D, R>) <= 227 * 1024, "fits");
+  if (ensure_smem_limit(tree_commit_kernel<D, R>, sizeof(CommitSmem<D, R>)) != cudaSuccess) return ZKV_ERR_CUDA;
+  const int64_t groups = ((int64_t)p.B * p.M + R - 1) / R;
+  tree_commit_kernel<D, R><<<dim3((unsigned)groups, (unsigned)p.Hkv, 2), kCommitThreads, sizeof(CommitSmem<D, R>), st>>>(p, rot);
   ZKV_CHECK_LAUNCH();
   if (launch_pdl(tree_commit_lengths_kernel, dim3((p.B + 127) / 128), dim3(128), 0, st, p) != cudaSuccess)
     return ZKV_ERR_CUDA;
   return ZKV_OK;
+}
+
+template <int D>
+static int launch_tree_commit(const zkv_tree_commit_params& p, cudaStream_t st) {
+  const bool many = ((int64_t)p.B * p.M + 15) / 16 * p.Hkv * 2 > 148;
+  return many ? launch_tree_commit_rows<D, 32>(p, st) : launch_tree_commit_rows<D, 16>(p, st);
 }
 
 }  // namespace zkv

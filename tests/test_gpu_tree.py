@@ -410,6 +410,9 @@ COMMITS = {
     "free slots behind a moved head": dict(B=2, N=6, M=6, Hkv=1, d=64, Sk=2, Sv=2, Tcap=32, W=5, state=[(7, 3, 2), (0, 4, 4)], accept=[6, 5]),
     "the same draft twice": dict(B=1, N=2, M=5, Hkv=1, d=64, Sk=2, Sv=2, Tcap=32, W=2, state=[(7, 2, 1)], accept=[5]),
     "many sequences": dict(B=37, N=5, M=5, Hkv=2, d=64, Sk=2, Sv=2, Tcap=32, W=4, state=[(i % 20, min(4, i % 6), i % 4 if i % 6 >= 4 else 0) for i in range(37)], accept=[(3 * i) % 6 for i in range(37)]),
+    "blocks of 32 evictions": dict(B=150, N=5, M=5, Hkv=4, d=64, Sk=2, Sv=1, Tcap=32, W=4, state=[(i % 20, 4, i % 4) for i in range(150)], accept=[(7 * i) % 6 for i in range(150)]),
+    "blocks of 32, d 256": dict(B=90, N=4, M=4, Hkv=4, d=256, Sk=1, Sv=2, Tcap=16, W=3, state=[(i % 12, 3, i % 3) for i in range(90)], accept=[(3 * i) % 5 for i in range(90)]),
+    "blocks of 32, d 128": dict(B=70, N=4, M=3, Hkv=6, d=128, Sk=3, Sv=2, Tcap=16, W=2, state=[(i % 12, 2, i % 2) for i in range(70)], accept=[(3 * i) % 4 for i in range(70)]),
     "eight stages": dict(B=2, N=3, M=3, Hkv=1, d=256, Sk=8, Sv=5, Tcap=16, W=2, state=[(7, 2, 1), (1, 2, 0)], accept=[3, 1]),
     "filled to the brim": dict(B=2, N=3, M=3, Hkv=1, d=64, Sk=2, Sv=2, Tcap=16, W=2, state=[(13, 2, 1), (16, 0, 0)], accept=[3, 2]),
 }
