@@ -1,6 +1,6 @@
 // Matrix products of fp16 tiles in shared memory with float32 accuracy (sm_100a).
 //
-// A float32 operand row is scaled by a power of two (its largest magnitude to 2^14 .. 2^15) and split
+// A float32 operand row is scaled by a power of two (its norm or largest magnitude to 2^14 .. 2^15) and split
 // into two fp16 planes, x = hi + lo with |x - hi - lo| <= 2^-23 |x| (fp16's subnormals end 2^-39
 // below the row's largest); a product is hi hi + hi lo + lo hi, three matrix instructions, and leaves
 // out lo lo <= 2^-22 of a term.  The tensor cores align the terms of a sum before they add, so a long
@@ -44,8 +44,9 @@ __device__ __forceinline__ void mma16816_zero(float (&d)[4], const uint32_t (&a)
 __device__ __forceinline__ void mma16816_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   float t[4];
   mma16816_zero(t, a, b0, b1);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] += t[i];
+  const float2 x = fadd2(make_float2(d[0], d[1]), make_float2(t[0], t[1]));
+  const float2 y = fadd2(make_float2(d[2], d[3]), make_float2(t[2], t[3]));
+  d[0] = x.x; d[1] = x.y; d[2] = y.x; d[3] = y.y;
 }
 
 // element (r, c) of a tile with K columns
@@ -78,10 +79,20 @@ __device__ __forceinline__ void frag_bt(uint32_t (&b)[4], const __half* t, int n
   ldsm4t(b, t + tile_at<N>(ks * 16 + (lane & 7) + 8 * ((lane >> 3) & 1), n0 + 8 * (lane >> 4)));
 }
 
-// The exponent e with |x| 2^-e in [2^14, 2^15) for a row's largest magnitude x, and 2^-e, 2^e
+// a lane that TransposeSum<N, N, 16> leaves the sum of value k with
+template <int N>
+__device__ __forceinline__ constexpr int sum_owner(int k) {
+  int lane = 0;
+  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2)
+    if (k & n) lane |= o;
+  return lane;
+}
+// The exponent e with x 2^-e in [2^14, 2^15) for a row's largest magnitude (or its norm: no element
+// is larger), and 2^e.  Rows below 2^-46 are scaled by 2^60: a norm whose squares underflow to zero
+// must not scale its elements beyond fp16.
 __device__ __forceinline__ int split_exponent(float largest) {
   int e = (int)((__float_as_uint(largest) >> 23) & 255u) - 127 - 14;
-  return e < -110 ? -110 : e;
+  return e < -60 ? -60 : e;
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ void split(float x, __half& hi, __half& lo) {

@@ -95,34 +95,44 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   if (real) {
     load(0);
     // the block's rows, rotated (float32 transform): warp w takes rows 8 w .. 8 w + 7
-    float v[8][E];
+    float v[8][E], part[8], down_of;
+    {
+      const int j = row0 + 8 * warp;
+      int b = j / a.RP, rho = j % a.RP, i = rho / a.G, g = rho % a.G;     // query i, head g of the group
 #pragma unroll
-    for (int k = 0; k < kQtRows / 8; ++k) {
-      const int j = row0 + 8 * warp + k, b = j / a.RP, rho = j % a.RP;
-      const bool there = b < a.B && rho < a.R && rho / a.G < present_queries(a.n_query, b, a.N);
-      const __half* qr = a.q + b * a.q_sb + (rho / a.G) * a.q_sn +
-                         ((int64_t)kvh * a.G + rho % a.G) * a.q_sh + lane;
+      for (int k = 0; k < 8; ++k) {
+        const bool there = b < a.B && rho < a.R && i < present_queries(a.n_query, b, a.N);
+        const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
+        for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
+        if (++g == a.G) g = 0, ++i;
+        if (++rho == a.RP) rho = i = g = 0, ++b;
+      }
     }
 #pragma unroll
-    for (int k = 0; k < kQtRows / 8; ++k) {
-      const int r = 8 * warp + k;
+    for (int k = 0; k < 8; ++k) {
       if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
         const float* l = a.k_smooth + (int64_t)kvh * D + lane;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[k][e] *= l[e * 32];
       }
       fwht_warp_f32<D>(v[k], lane);
-      float big = 0.f;
+      part[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[k][e]));
-      const int ex = split_exponent(warp_max_f32(big));
-      const float down = exp2_int(-ex);
-      if (lane == 0) sm.qs[r] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+      for (int e = 0; e < E; ++e) part[k] = fmaf(v[k][e], v[k][e], part[k]);
+    }
+    {
+      int own = 0;        // the norms of the eight rows at once
+      const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
+      down_of = exp2_int(-ex);
+      sm.qs[8 * warp + own] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int at = tile_at<D>(r, e * 32 + lane);
+        const int at = tile_at<D>(8 * warp + k, e * 32 + lane);
         split(v[k][e] * down, sm.q[0][at], sm.q[1][at]);
       }
     }
@@ -146,15 +156,23 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
       for (int i = 0; i < 4; ++i) acc[n][i] = cross[n][i] = 0.f;
     if (real) {
       __syncthreads();              // the previous chunk has been read
+      float part[8], down_of;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        part[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[k] = fmaf(cw[k][e], cw[k][e], part[k]);
+      }
+      {
+        int own = 0;
+        const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
+        down_of = exp2_int(-ex);
+        sm.cs[8 * warp + own] = exp2_int(ex);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int c = 8 * warp + k;
-        float big = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(cw[k][e]));
-        const int ex = split_exponent(warp_max_f32(big));
-        const float down = exp2_int(-ex);
-        if (lane == 0) sm.cs[c] = exp2_int(ex);
+        const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
         alignas(16) __half hi[E], lo[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
@@ -206,6 +224,33 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
         }
     }
   }
+}
+
+// Table gathers and counter additions take the permuted bytes [column | code] of a packed code word as
+// a shared-memory address with the start of the tables as an immediate offset: dynamic shared memory begins at kTableBase, behind the
+// reserved system area (the kernel checks it and reports ZKV_DEVERR_SMEM otherwise).  No memory
+// clobber: tables and counters are written and read on either side of a barrier.
+constexpr int kTableBase = 1024;
+__device__ __forceinline__ float2 lds_pair(uint32_t x) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2+%3];" : "=f"(v.x), "=f"(v.y) : "r"(x), "n"(kTableBase));
+  return v;
+}
+__device__ __forceinline__ float4 lds_quad(uint32_t x) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4+%5];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(x), "n"(kTableBase));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ void red_counter(uint32_t x, uint32_t u) {
+  asm volatile("red.shared.add.u32 [%0+%2], %1;" ::"r"(x), "r"(u), "n"(kTableBase + OFF));
+}
+
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
+  return d;
 }
 
 // The code rows of one (sequence, kv head): contiguous or paged.

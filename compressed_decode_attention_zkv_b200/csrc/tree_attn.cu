@@ -402,27 +402,6 @@ struct TreeScan {
   static constexpr int KW = SKP <= 4 ? 1 : 2, VW = SVP <= 4 ? 1 : 2;   // code words per token
 };
 
-// Gathers and counter additions take the permuted bytes as a shared-memory address with the start of
-// the tables as an immediate offset: dynamic shared memory begins at kTreeSmemBase, behind the
-// reserved system area (the kernel checks it and reports ZKV_DEVERR_SMEM otherwise).  No memory
-// clobber: tables and counters are written and read on either side of a barrier.
-constexpr int kTreeSmemBase = 1024;
-__device__ __forceinline__ float2 tree_lds(uint32_t x) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2+%3];" : "=f"(v.x), "=f"(v.y) : "r"(x), "n"(kTreeSmemBase));
-  return v;
-}
-template <int OFF>
-__device__ __forceinline__ void tree_red(uint32_t x, uint32_t u) {
-  asm volatile("red.shared.add.u32 [%0+%2], %1;" ::"r"(x), "r"(u), "n"(kTreeSmemBase + OFF));
-}
-
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(s));
-  return d;
-}
-
 // The codes of four tokens from the warp's copy (p: the first one's S bytes; 4-byte aligned).  EXACT:
 // rows are SP bytes.
 template <int SP, int W, bool EXACT>
@@ -514,7 +493,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
   int64_t lo = blockIdx.x * per;
   const int64_t hi = lo + per < total ? lo + per : total;
   if (lo >= hi) return;
-  if ((uint32_t)__cvta_generic_to_shared(sm) != kTreeSmemBase) {   // (the slots stay unwritten)
+  if ((uint32_t)__cvta_generic_to_shared(sm) != kTableBase) {   // (the slots stay unwritten)
     if (tid == 0) set_error(a.err, ZKV_DEVERR_SMEM);
     return;
   }
@@ -577,7 +556,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       for (int i = 0; i < C::KW; ++i) x[i] = byte_perm(w[i], 0u, korder);
 #pragma unroll
       for (int i = 0; i < SKP; ++i)
-        s = fadd2(s, tree_lds(byte_perm(x[i < 4 ? 0 : C::KW - 1], kcol[i / 2],
+        s = fadd2(s, lds_pair(byte_perm(x[i < 4 ? 0 : C::KW - 1], kcol[i / 2],
                                         (4u + (i & 1)) | ((i & 3u) << 4) | 0x7600u)));
       return s;
     };
@@ -741,8 +720,8 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
 #pragma unroll
           for (int i = 0; i < SVP; ++i) {
             const uint32_t y = x[i < 4 ? 0 : C::VW - 1], sel = (4u + (i & 1)) | ((i & 3u) << 4) | 0x7600u;
-            tree_red<C::VOFF>(byte_perm(y, vcol[0][i / 2], sel), ua);
-            tree_red<C::VOFF>(byte_perm(y, vcol[1][i / 2], sel), ub);
+            red_counter<C::VOFF>(byte_perm(y, vcol[0][i / 2], sel), ua);
+            red_counter<C::VOFF>(byte_perm(y, vcol[1][i / 2], sel), ub);
           }
         }
       }
@@ -865,15 +844,23 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
       for (int k = 0; k < 8; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) v[k][e] = __ldg(C + (int64_t)(8 * (k0 + k) + warp) * D + e);
+      float part[8], down_of;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        part[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[k] = fmaf(v[k][e], v[k][e], part[k]);
+      }
+      {
+        int own = 0;      // the norms of the eight codewords at once
+        const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
+        down_of = exp2_int(-ex);
+        sm.cs[8 * (k0 + own) + warp] = exp2_int(ex);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int c = 8 * (k0 + k) + warp;
-        float big = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(v[k][e]));
-        const int ex = split_exponent(warp_max_f32(big));
-        const float down = exp2_int(-ex);
-        if (lane == 0) sm.cs[c] = exp2_int(ex);
+        const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
           alignas(4) __half hi[2], lo[2];

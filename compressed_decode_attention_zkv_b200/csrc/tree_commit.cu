@@ -104,15 +104,6 @@ struct CommitSmem {
   int64_t warp_sum[kCommitThreads / 32];
 };
 
-// a lane that TransposeSum<N, N, 16> leaves the sum of value k with
-template <int N>
-__device__ __forceinline__ constexpr int owner(int k) {
-  int lane = 0;
-  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2)
-    if (k & n) lane |= o;
-  return lane;
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_commit_params p, double rot) {
   constexpr int E = D / 32, CH = CommitSmem<D, R>::CH, NC = kCodebook / CH, CW = CH / 16;   // CW: codewords per warp
@@ -256,7 +247,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
 #pragma unroll
         for (int k = 0; k < CW; ++k) {
           const int c = CW * warp + k;
-          const float down = __shfl_sync(0xffffffffu, down_of, owner<CW>(k));
+          const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<CW>(k));
           alignas(16) __half hi[E], lo[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);

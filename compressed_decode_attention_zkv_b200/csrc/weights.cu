@@ -7,14 +7,16 @@
 //   acc[b][kvh][t] += sum over the rows rho of (b, kvh) of 2^(score_rho[t] - lse_rho log2 e)
 //
 // Two kernels: the key lookup tables of every row (query_tables.cuh), then the scan.  A scan block
-// takes kWtTok tokens of one (sequence, kv head), kWtTU per thread, through all row groups: each
-// token's total stays in a register and is added to memory once, by one thread.  Every token is
+// takes kWtTok tokens of one (sequence, kv head) at a time, kWtTU per thread, through all row groups
+// (one group's tables are loaded once for all its tokens): each token's total stays in a register and
+// is added to memory once, by one thread.  As many blocks as are resident at once share the tokens.  Every token is
 // read and written by exactly one thread, so the result does not depend on any order.
 //
-// Shared memory: the tables of one group of RG rows, a row of RB bytes per codeword.  A thread
-// reads 16 bytes (four rows) at a time.  The eight lanes of a 16-byte phase visit eight distinct
-// columns of the codeword's row (they start at different stages, row halves or table copies), so a
-// gather has no bank conflict whatever the codes are.
+// Shared memory: the tables of one group of RG rows, a row of 128 bytes or more (copies of smaller ones)
+// every 256 bytes per codeword, so that a gather's address is one byte permutation of the packed codes.  A thread reads 16 bytes
+// (four rows) at a time.  The eight lanes of a 16-byte phase visit eight distinct 16-byte columns,
+// modulo 128 bytes, of their codewords' rows (they start at different stages, row halves or copies),
+// so a gather has no bank conflict whatever the codes are.
 #include "query_tables.cuh"
 
 #include <cmath>
@@ -50,18 +52,18 @@ __global__ void __launch_bounds__(kQtThreads) weights_tables_kernel(WeightArgs a
 template <int SKP, int RG>
 struct WtCfg {
   static constexpr int NH = RG / 4;                                   // 16-byte halves
-  static constexpr int CP = SKP * NH >= 8 ? 1 : 8 / (SKP * NH);       // table copies
-  static constexpr int RB = SKP * NH * CP * 16;                       // bytes per codeword
+  static constexpr int PC = SKP * NH > 8 ? SKP * NH : 8;              // 16-byte pieces of a row
+  static constexpr int CP = PC / (SKP * NH);                          // table copies
   static constexpr int LS = SKP < 8 / NH ? SKP : 8 / NH;              // stages that lanes start at
-  static constexpr int SMEM = kCodebook * RB;
+  static constexpr int SMEM = kCodebook * 256 + RG * 4;
   static constexpr int KW = SKP <= 4 ? 1 : 2;
 };
 
 template <int SKP, int RG>
-__global__ void __launch_bounds__(kWtThreads) weights_scan_kernel(WeightArgs a) {
+__global__ void __launch_bounds__(kWtThreads, 2) weights_scan_kernel(WeightArgs a) {
   using C = WtCfg<SKP, RG>;
   extern __shared__ __align__(16) unsigned char sm[];
-  __shared__ float ls[RG];                        // -lse in base 2; -inf: the row counts for nothing
+  float* ls = reinterpret_cast<float*>(sm + kCodebook * 256);   // -lse in base 2; -inf: counts for nothing
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t pair = blockIdx.y;
   const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv);
@@ -71,87 +73,140 @@ __global__ void __launch_bounds__(kWtThreads) weights_scan_kernel(WeightArgs a) 
     n = n < 0 ? 0 : a.Tcap;
   }
   if (n > a.max_comp) n = a.max_comp;
-  const int64_t t0 = (int64_t)blockIdx.x * kWtTok + tid;
-  const bool idle = (int64_t)blockIdx.x * kWtTok >= n;
   const CodeRows kr = code_rows(a.k_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh, a.Hkv,
                                 a.Tcap, a.Sk, a.err);
+  // this thread's tokens: t0 + u kWtThreads.  Their codes are in flight across the wait for the tables
+  // (that kernel does not write them) and beside the last tokens' additions.  A thread behind the last
+  // token takes that one's and adds nothing.
+  int64_t t0 = (int64_t)blockIdx.x * kWtTok + tid;
   uint32_t w[kWtTU][C::KW];
-  float sum[kWtTU];
+  const bool word = !a.table && SKP >= 2 && a.Sk == SKP;        // one aligned machine word per token
+  auto load = [&]() {
+    if (t0 - tid >= n) return;
+    if (word) {
 #pragma unroll
-  for (int u = 0; u < kWtTU; ++u) {
-    sum[u] = 0.f;
+      for (int u = 0; u < kWtTU; ++u) {
+        const int64_t t = t0 + u * kWtThreads;
+        const uint8_t* p = kr.base + (t < n ? t : n - 1) * SKP;
+        if constexpr (SKP == 2) {
+          w[u][0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        } else if constexpr (SKP == 4) {
+          w[u][0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+        } else if constexpr (SKP == 8) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          w[u][0] = x.x;
+          w[u][C::KW - 1] = x.y;
+        }
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < C::KW; ++i) w[u][i] = 0u;
-    const int64_t t = t0 + u * kWtThreads;
-    if (t < n) load_codes<SKP>(kr, (uint32_t)t, a.Sk, w[u]);
-  }
-  // this lane's columns: starting half, stage and copy
+      for (int u = 0; u < kWtTU; ++u) {
+        const int64_t t = t0 + u * kWtThreads;
+        load_codes<SKP>(kr, (uint32_t)(t < n ? t : n - 1), a.Sk, w[u]);
+      }
+    }
+  };
+  load();
+  // this lane's columns: starting half, stage and copy; the order that a code word's bytes are put in
   const int l8 = lane & 7;
   const int lh = l8 & (C::NH - 1), lst = (l8 / C::NH) & (C::LS - 1);
   const int lc = C::CP > 1 ? l8 / (C::NH * C::LS) : 0;
-  pdl_wait();
-  if (idle) return;
-  for (int rg = 0; rg < a.NRG; ++rg) {
-    __syncthreads();
-    if (tid < RG) {
-      const int rho = rg * RG + tid;
-      float x = -INFINITY;
-      if (rho < a.qt.R) {
-        const float l = a.lse[((int64_t)b * a.N + rho / a.G) * (a.Hkv * a.G) + (int64_t)kvh * a.G + rho % a.G];
-        if (fabsf(l) < INFINITY) x = -l * kLog2e;
-      }
-      ls[tid] = x;
-    }
-    __syncthreads();
-    // tables; those of rows that count for nothing are zero (their queries may hold anything)
-    const float* src = a.qt.lut + (pair * a.NRG + rg) * (int64_t)(kCodebook * SKP * RG);
-    constexpr int Q = SKP * C::NH;
-    for (int f = tid; f < kCodebook * Q; f += kWtThreads) {
-      const int c = f / Q, q = f % Q, r4 = 4 * (q & (C::NH - 1));
-      float4 v = *reinterpret_cast<const float4*>(src + (int64_t)f * 4);
-      if (ls[r4] == -INFINITY) v.x = 0.f;
-      if (ls[r4 + 1] == -INFINITY) v.y = 0.f;
-      if (ls[r4 + 2] == -INFINITY) v.z = 0.f;
-      if (ls[r4 + 3] == -INFINITY) v.w = 0.f;
+  uint32_t col[C::NH][(SKP + 1) / 2], order = 0u;
 #pragma unroll
-      for (int k = 0; k < C::CP; ++k)
-        *reinterpret_cast<float4*>(sm + c * C::RB + 16 * (q * C::CP + k)) = v;
-    }
-    __syncthreads();
-    float init[C::NH][4];
+  for (int x = 0; x < C::NH; ++x)
+#pragma unroll
+    for (int i = 0; i < (SKP + 1) / 2; ++i) col[x][i] = 0u;
+#pragma unroll
+  for (int i = 0; i < SKP; ++i) {
+    const int st = i ^ lst;
 #pragma unroll
     for (int x = 0; x < C::NH; ++x)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) init[x][q] = ls[4 * (x ^ lh) + q];
-#pragma unroll
-    for (int u = 0; u < kWtTU; ++u) {
-      float s[C::NH][4];
-#pragma unroll
-      for (int x = 0; x < C::NH; ++x)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s[x][q] = init[x][q];
-#pragma unroll
-      for (int i = 0; i < SKP; ++i) {
-        const int st = i ^ lst;
-        const uint32_t word = SKP <= 4 ? w[u][0] : ((st >> 2) ? w[u][C::KW - 1] : w[u][0]);
-        const uint32_t c = (word >> (8 * (st & 3))) & 255u;
-#pragma unroll
-        for (int x = 0; x < C::NH; ++x) {
-          const float4 v = *reinterpret_cast<const float4*>(
-              sm + c * C::RB + 16 * ((st * C::NH + (x ^ lh)) * C::CP + lc));
-          s[x][0] += v.x; s[x][1] += v.y; s[x][2] += v.z; s[x][3] += v.w;
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < C::NH; ++x)
-        sum[u] += (ex2_approx(s[x][0]) + ex2_approx(s[x][1])) + (ex2_approx(s[x][2]) + ex2_approx(s[x][3]));
-    }
+      col[x][i / 2] |= (uint32_t)(16 * ((st * C::NH + (x ^ lh)) * C::CP + lc)) << (8 * (i & 1));
+    if (i < 4) order |= (uint32_t)(st & 3) << (4 * i);
   }
-  float* acc = a.acc + pair * a.Tcap;
+  const bool cross = (lst & 4) != 0;           // (8 stages: the second word comes first)
+  pdl_wait();
+  if (t0 - tid >= n) return;
+  if ((uint32_t)__cvta_generic_to_shared(sm) != kTableBase) {
+    if (tid == 0) set_error(a.err, ZKV_DEVERR_SMEM);
+    return;
+  }
+  bool loaded = false;
+  while (t0 - tid < n) {
+    float sum[kWtTU];
 #pragma unroll
-  for (int u = 0; u < kWtTU; ++u) {
-    const int64_t t = t0 + u * kWtThreads;
-    if (t < n) acc[t] += sum[u];
+    for (int u = 0; u < kWtTU; ++u) sum[u] = 0.f;
+    for (int rg = 0; rg < a.NRG; ++rg) {
+      if (a.NRG > 1 || !loaded) {
+        loaded = true;
+        __syncthreads();
+        if (tid < RG) {
+          const int rho = rg * RG + tid;
+          float x = -INFINITY;
+          if (rho < a.qt.R) {
+            const float l = a.lse[((int64_t)b * a.N + rho / a.G) * (a.Hkv * a.G) + (int64_t)kvh * a.G + rho % a.G];
+            if (fabsf(l) < INFINITY) x = -l * kLog2e;
+          }
+          ls[tid] = x;
+        }
+        __syncthreads();
+        // tables; those of rows that count for nothing are zero (their queries may hold anything)
+        const float* src = a.qt.lut + (pair * a.NRG + rg) * (int64_t)(kCodebook * SKP * RG);
+        // thread = one 16-byte piece of a codeword's row: whole rows are written, no bank conflict
+        constexpr int PER = kWtThreads / C::PC, TURNS = kCodebook / PER;
+        const int piece = tid % C::PC, q = piece / C::CP, r4 = 4 * (q & (C::NH - 1));
+        const bool dead[4] = {ls[r4] == -INFINITY, ls[r4 + 1] == -INFINITY, ls[r4 + 2] == -INFINITY, ls[r4 + 3] == -INFINITY};
+#pragma unroll
+        for (int k0 = 0; k0 < TURNS; k0 += 4) {
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = *reinterpret_cast<const float4*>(src + ((tid / C::PC + (k0 + k) * PER) * SKP * C::NH + q) * 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(sm + (tid / C::PC + (k0 + k) * PER) * 256 + 16 * piece) =
+              make_float4(dead[0] ? 0.f : v[k].x, dead[1] ? 0.f : v[k].y, dead[2] ? 0.f : v[k].z, dead[3] ? 0.f : v[k].w);
+        }
+        __syncthreads();
+      }
+      float2 init[C::NH][2];
+#pragma unroll
+      for (int x = 0; x < C::NH; ++x)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          init[x][q] = *reinterpret_cast<const float2*>(ls + 4 * (x ^ lh) + 2 * q);
+#pragma unroll
+      for (int u = 0; u < kWtTU; ++u) {
+        float2 s[C::NH][2];
+#pragma unroll
+        for (int x = 0; x < C::NH; ++x) s[x][0] = init[x][0], s[x][1] = init[x][1];
+        uint32_t y[C::KW];
+#pragma unroll
+        for (int i = 0; i < C::KW; ++i)
+          y[i] = byte_perm(C::KW > 1 && cross ? w[u][C::KW - 1 - i] : w[u][i], 0u, order);
+#pragma unroll
+        for (int i = 0; i < SKP; ++i)
+#pragma unroll
+          for (int x = 0; x < C::NH; ++x) {
+            const float4 v = lds_quad(byte_perm(y[i < 4 ? 0 : C::KW - 1], col[x][i / 2],
+                                                (4u + (i & 1)) | ((i & 3u) << 4) | 0x7600u));
+            s[x][0] = fadd2(s[x][0], make_float2(v.x, v.y));
+            s[x][1] = fadd2(s[x][1], make_float2(v.z, v.w));
+          }
+#pragma unroll
+        for (int x = 0; x < C::NH; ++x)
+          sum[u] += (ex2_ftz(s[x][0].x) + ex2_ftz(s[x][0].y)) + (ex2_ftz(s[x][1].x) + ex2_ftz(s[x][1].y));
+      }
+    }
+    float* acc = a.acc + pair * a.Tcap + t0;
+    const int left = (int)(n - t0 < 0 ? 0 : n - t0 < kWtTok ? n - t0 : kWtTok);
+    t0 += (int64_t)gridDim.x * kWtTok;
+    load();
+#pragma unroll
+    for (int u = 0; u < kWtTU; ++u) sum[u] += u * kWtThreads < left ? acc[u * kWtThreads] : 0.f;
+#pragma unroll
+    for (int u = 0; u < kWtTU; ++u)
+      if (u * kWtThreads < left) acc[u * kWtThreads] = sum[u];
   }
 }
 
@@ -243,7 +298,10 @@ extern "C" int zkv_rvq_accumulate_weights(const zkv_weights_params* p, void* wor
   cudaError_t e = p->d == 64 ? launch_weights_tables<64>(a, st)
                 : p->d == 128 ? launch_weights_tables<128>(a, st) : launch_weights_tables<256>(a, st);
   if (e != cudaSuccess) return ZKV_ERR_CUDA;
-  const dim3 grid((unsigned)((p->max_comp_len + kWtTok - 1) / kWtTok), (unsigned)(p->B * p->Hkv));
+  // two blocks per SM are resident
+  const int64_t pairs = (int64_t)p->B * p->Hkv, chunks = (p->max_comp_len + kWtTok - 1) / kWtTok;
+  const int64_t share = 296 / pairs < 1 ? 1 : 296 / pairs;
+  const dim3 grid((unsigned)(chunks < share ? chunks : share), (unsigned)pairs);
   if (RG == 4) {
     e = q.SKP == 1 ? launch_weights_scan<1, 4>(a, grid, st) : q.SKP == 2 ? launch_weights_scan<2, 4>(a, grid, st)
       : q.SKP == 4 ? launch_weights_scan<4, 4>(a, grid, st) : launch_weights_scan<8, 4>(a, grid, st);
