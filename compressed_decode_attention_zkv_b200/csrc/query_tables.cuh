@@ -94,30 +94,27 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   };
   if (real) {
     load(0);
-    // the block's rows, rotated (float32 transform): warp w takes rows 8 w .. 8 w + 7
+    // the block's rows, rotated (float32 transform): warp w takes rows w, w + 8, ...
+    const int rows = a.B * a.RP - row0;          // rows from here on
     float v[8][E], part[8], down_of;
-    {
-      const int j = row0 + 8 * warp;
-      int b = j / a.RP, rho = j % a.RP, i = rho / a.G, g = rho % a.G;     // query i, head g of the group
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool there = b < a.B && rho < a.R && i < present_queries(a.n_query, b, a.N);
-        const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
+    for (int k = 0; k < 8; ++k) {
+      const int j = row0 + warp + 8 * k, b = j / a.RP, rho = j % a.RP, i = rho / a.G, g = rho % a.G;
+      const bool there = warp + 8 * k < rows && rho < a.R && i < present_queries(a.n_query, b, a.N);
+      const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
-        if (++g == a.G) g = 0, ++i;
-        if (++rho == a.RP) rho = i = g = 0, ++b;
-      }
+      for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      part[k] = 0.f;
+      if (warp + 8 * k >= rows) continue;
       if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
         const float* l = a.k_smooth + (int64_t)kvh * D + lane;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[k][e] *= l[e * 32];
       }
       fwht_warp_f32<D>(v[k], lane);
-      part[k] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) part[k] = fmaf(v[k][e], v[k][e], part[k]);
     }
@@ -125,19 +122,22 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
       int own = 0;        // the norms of the eight rows at once
       const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
       down_of = exp2_int(-ex);
-      sm.qs[8 * warp + own] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+      sm.qs[warp + 8 * own] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int at = tile_at<D>(8 * warp + k, e * 32 + lane);
+        const int at = tile_at<D>(warp + 8 * k, e * 32 + lane);
         split(v[k][e] * down, sm.q[0][at], sm.q[1][at]);
       }
     }
   }
-  const int wr = warp & 3, wc = warp >> 2;      // rows 16 wr .., codewords 32 wc .. of the chunk
+  // products: rows 16 wr .. of the block x codewords 8 NT wc .. of the chunk per warp; with at most 16
+  // rows all warps share their codewords
+  const bool few = (int64_t)a.B * a.RP - row0 <= 16;
+  const int wr = few ? 0 : warp & 3, cl0 = few ? 8 * warp : 32 * (warp >> 2);
   const int g = lane >> 2, t4 = lane & 3;
   // this thread's two rows in the tables (null: behind the last)
   float* out[2];
@@ -148,12 +148,20 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
                                    ((int64_t)kCodebook * a.SKP * a.RG) + rho % a.RG
                      : nullptr;
   }
+  auto put = [&](int chunk, int n, const float (&acc)[4], const float (&cross)[4]) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (!out[q]) continue;
+      const float qs = real ? sm.qs[16 * wr + g + 8 * q] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int cl = cl0 + 8 * n + 2 * t4 + i;
+        const float x = real ? (acc[2 * q + i] + cross[2 * q + i]) * sm.cs[cl] * qs : 0.f;
+        out[q][((int64_t)(c0 + chunk * kQtCodes + cl) * a.SKP + s) * a.RG] = x;
+      }
+    }
+  };
   for (int chunk = 0; chunk < chunks; ++chunk) {
-    float acc[4][4], cross[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = cross[n][i] = 0.f;
     if (real) {
       __syncthreads();              // the previous chunk has been read
       float part[8], down_of;
@@ -191,37 +199,53 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
       }
       __syncthreads();
       if (chunk + 1 < chunks) load(chunk + 1);
+    }
+    if (few) {
+      float acc[4] = {}, cross[2][4] = {};
+      if (real) {
 #pragma unroll 2
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t ah[4], al[4];
-        frag_a<D>(ah, sm.q[0], 16 * wr, ks, lane);
-        frag_a<D>(al, sm.q[1], 16 * wr, ks, lane);
-#pragma unroll
-        for (int n = 0; n < 4; n += 2) {
+        for (int ks = 0; ks < D / 16; ks += 2) {
           uint32_t bh[4], bl[4];
-          frag_b<D>(bh, sm.c[0], 32 * wc + 8 * n, ks, lane);
-          frag_b<D>(bl, sm.c[1], 32 * wc + 8 * n, ks, lane);
-          mma16816_add(acc[n], ah, bh[0], bh[1]);
-          mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
-          mma16816(cross[n], ah, bl[0], bl[1]);
-          mma16816(cross[n + 1], ah, bl[2], bl[3]);
-          mma16816(cross[n], al, bh[0], bh[1]);
-          mma16816(cross[n + 1], al, bh[2], bh[3]);
+          frag_b2<D>(bh, sm.c[0], cl0, ks, lane);
+          frag_b2<D>(bl, sm.c[1], cl0, ks, lane);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t ah[4], al[4];
+            frag_a<D>(ah, sm.q[0], 0, ks + i, lane);
+            frag_a<D>(al, sm.q[1], 0, ks + i, lane);
+            mma16816_add(acc, ah, bh[2 * i], bh[2 * i + 1]);
+            mma16816(cross[0], ah, bl[2 * i], bl[2 * i + 1]);
+            mma16816(cross[1], al, bh[2 * i], bh[2 * i + 1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cross[0][i] += cross[1][i];
+      }
+      put(chunk, 0, acc, cross[0]);
+    } else {
+      float acc[4][4] = {}, cross[4][4] = {};
+      if (real) {
+#pragma unroll 2
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t ah[4], al[4];
+          frag_a<D>(ah, sm.q[0], 16 * wr, ks, lane);
+          frag_a<D>(al, sm.q[1], 16 * wr, ks, lane);
+#pragma unroll
+          for (int n = 0; n < 4; n += 2) {
+            uint32_t bh[4], bl[4];
+            frag_b<D>(bh, sm.c[0], cl0 + 8 * n, ks, lane);
+            frag_b<D>(bl, sm.c[1], cl0 + 8 * n, ks, lane);
+            mma16816_add(acc[n], ah, bh[0], bh[1]);
+            mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
+            mma16816(cross[n], ah, bl[0], bl[1]);
+            mma16816(cross[n + 1], ah, bl[2], bl[3]);
+            mma16816(cross[n], al, bh[0], bh[1]);
+            mma16816(cross[n + 1], al, bh[2], bh[3]);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (!out[q]) continue;
-      const float qs = real ? sm.qs[16 * wr + g + 8 * q] : 0.f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int cl = 32 * wc + 8 * n + 2 * t4 + i;
-          const float x = real ? (acc[n][2 * q + i] + cross[n][2 * q + i]) * sm.cs[cl] * qs : 0.f;
-          out[q][((int64_t)(c0 + chunk * kQtCodes + cl) * a.SKP + s) * a.RG] = x;
-        }
+      for (int n = 0; n < 4; ++n) put(chunk, n, acc[n], cross[n]);
     }
   }
 }

@@ -968,9 +968,11 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
   }
   __syncthreads();
   const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
-  const int wr = warp & 3, wc = warp >> 2, g = lane >> 2, t4 = lane & 3;
-  if (sm.row[2 * wr] >= 0 || sm.row[2 * wr + 1] >= 0) {
-    constexpr int NT = D / 16;                 // output tiles of 8 dimensions
+  const int g = lane >> 2, t4 = lane & 3;
+  // rows 16 wr .. x 8 NT dimensions from d0 per warp; with at most two items all warps share theirs
+  auto product = [&](auto tiles, int wr, int d0) {
+    constexpr int NT = decltype(tiles)::value;
+    if (sm.row[2 * wr] < 0 && sm.row[2 * wr + 1] < 0) return;
     float acc[NT][4], cross[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -981,17 +983,27 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
       uint32_t ah[4], al[4];
       frag_at<64>(ah, sm.w[0], 16 * wr, ks, lane);
       frag_at<64>(al, sm.w[1], 16 * wr, ks, lane);
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
+      if constexpr (NT == 1) {
         uint32_t bh[4], bl[4];
-        frag_bt<D>(bh, sm.cv[0], wc * (D / 2) + 8 * n, ks, lane);
-        frag_bt<D>(bl, sm.cv[1], wc * (D / 2) + 8 * n, ks, lane);
-        mma16816_add(acc[n], ah, bh[0], bh[1]);
-        mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
-        mma16816(cross[n], ah, bl[0], bl[1]);
-        mma16816(cross[n + 1], ah, bl[2], bl[3]);
-        mma16816(cross[n], al, bh[0], bh[1]);
-        mma16816(cross[n + 1], al, bh[2], bh[3]);
+        frag_bt<D>(bh, sm.cv[0], d0 & ~15, ks, lane);      // (both halves of 16 dimensions: one is used)
+        frag_bt<D>(bl, sm.cv[1], d0 & ~15, ks, lane);
+        const bool up = d0 & 8;
+        mma16816_add(acc[0], ah, up ? bh[2] : bh[0], up ? bh[3] : bh[1]);
+        mma16816(cross[0], ah, up ? bl[2] : bl[0], up ? bl[3] : bl[1]);
+        mma16816(cross[0], al, up ? bh[2] : bh[0], up ? bh[3] : bh[1]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t bh[4], bl[4];
+          frag_bt<D>(bh, sm.cv[0], d0 + 8 * n, ks, lane);
+          frag_bt<D>(bl, sm.cv[1], d0 + 8 * n, ks, lane);
+          mma16816_add(acc[n], ah, bh[0], bh[1]);
+          mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
+          mma16816(cross[n], ah, bl[0], bl[1]);
+          mma16816(cross[n + 1], ah, bl[2], bl[3]);
+          mma16816(cross[n], al, bh[0], bh[1]);
+          mma16816(cross[n + 1], al, bh[2], bh[3]);
+        }
       }
     }
 #pragma unroll
@@ -999,13 +1011,15 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
       const int64_t row = sm.row[2 * wr + q];
       if (row < 0) continue;
       const float ws = sm.ws[16 * wr + 8 * q + g];
-      float* o = a.parts + (part * rows + row + g) * D + wc * (D / 2) + 2 * t4;
+      float* o = a.parts + (part * rows + row + g) * D + d0 + 2 * t4;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         *reinterpret_cast<float2*>(o + 8 * n) = make_float2((acc[n][2 * q] + cross[n][2 * q]) * ws,
                                                             (acc[n][2 * q + 1] + cross[n][2 * q + 1]) * ws);
     }
-  }
+  };
+  if ((int64_t)a.B * a.NRG - group * 8 <= 2) product(std::integral_constant<int, D / 64>{}, 0, warp * (D / 8));
+  else product(std::integral_constant<int, D / 16>{}, warp & 3, (warp >> 2) * (D / 2));
 }
 
 // ---------------------------------------------------------------------------------------------
