@@ -11,7 +11,8 @@
 // (mma_split.cuh).  Block = 64 rows of one kv head (rows of several sequences side by side: they
 // share the codewords) x one stage; it rotates its rows once and takes the codewords in chunks of
 // 64, the next chunk's loads in flight during a chunk's products.  With few blocks the chunks of a
-// stage are shared out over 2 or 4 blocks.
+// stage are shared out over 2 or 4 blocks.  The codewords are split in the block, or, where many
+// blocks would repeat that, come split from a kernel before (SplitBooks).
 #pragma once
 
 #include "mma_split.cuh"
@@ -19,6 +20,13 @@
 namespace zkv {
 
 constexpr int kQtRows = 64, kQtCodes = 64, kQtThreads = 256;
+
+// Codewords split into fp16 planes once (mma_split.cuh): [row][D] each, row = (kv head, stage, codeword)
+struct SplitBooks {
+  __half *hi, *lo;
+  float* scale;            // [row] 2^e
+};
+inline size_t split_books_bytes(int64_t rows, int D) { return (size_t)rows * D * 4; }
 
 struct QueryTables {
   int B, N, G, Hkv, Sk, SKP, RG;
@@ -32,6 +40,7 @@ struct QueryTables {
   float scale_log2;
   double rot;
   float* lut;     // [B * Hkv][RP / RG][256][SKP][RG]
+  SplitBooks books;         // of Ck, or null planes
 
   __host__ __device__ int row_blocks() const { return (int)(((int64_t)B * RP + kQtRows - 1) / kQtRows); }
   // blocks that share the chunks of a stage: at least one block per SM where the chunks allow it
@@ -52,16 +61,62 @@ __device__ __forceinline__ int present_queries(const int32_t* n, int b, int N) {
   return v < 0 ? 0 : v > N ? N : v;
 }
 
+// 64 rows of a split book into a tile of the two planes (asynchronous)
 template <int D>
+__device__ __forceinline__ void copy_split(const SplitBooks& books, int64_t row0, int rows, __half* hi, __half* lo,
+                                           int threads) {
+  for (int f = threadIdx.x; f < rows * (D / 8); f += threads) {
+    const int r = f / (D / 8), c = (f % (D / 8)) * 8, at = tile_at<D>(r, c);
+    cp_async16(hi + at, books.hi + (row0 + r) * D + c);
+    cp_async16(lo + at, books.lo + (row0 + r) * D + c);
+  }
+}
+
+// Splits 64 rows of [row][D] float32 codewords: warp w takes rows 8 w .. 8 w + 7, lane = D / 32
+// dimensions in a row
+template <int D>
+__device__ __forceinline__ void split_books_block(const float* src, const SplitBooks& books, int64_t row0) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = row0 + 8 * warp;
+  float v[8][E], part[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    part[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[k][e] = __ldg(src + (first + k) * D + lane * E + e);
+      part[k] = fmaf(v[k][e], v[k][e], part[k]);
+    }
+  }
+  int own = 0;
+  const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
+  const float down_of = exp2_int(-ex);
+  books.scale[first + own] = exp2_int(ex);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      __half2 hi, lo;
+      split(v[k][e] * down, hi.x, lo.x);
+      split(v[k][e + 1] * down, hi.y, lo.y);
+      *reinterpret_cast<__half2*>(books.hi + (first + k) * D + lane * E + e) = hi;
+      *reinterpret_cast<__half2*>(books.lo + (first + k) * D + lane * E + e) = lo;
+    }
+  }
+}
+
+template <int D, bool SPLIT>
 struct QtSmem {
   __half q[2][kQtRows * D];       // rotated queries: high and low plane
-  __half c[2][kQtCodes * D];      // codewords
+  __half c[SPLIT ? 2 : 1][2][kQtCodes * D];      // codewords (split before: two chunks in flight)
   float qs[kQtRows];              // their scales (softmax scale included)
   float cs[kQtCodes];
 };
 
-template <int D>
-__device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t blk, QtSmem<D>& sm) {
+template <int D, bool SPLIT>
+__device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t blk, QtSmem<D, SPLIT>& sm) {
   constexpr int E = D / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int shares = a.shares(), chunks = kCodebook / kQtCodes / shares;
@@ -75,8 +130,15 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   const bool real = s < a.Sk;
   // warp w loads codewords 8 w .. 8 w + 7 of a chunk, lane = E dimensions in a row
   float cw[8][E];
+  const int64_t book0 = ((int64_t)kvh * a.Sk + s) * kCodebook + c0;      // the block's first codeword
   auto load = [&](int chunk) {
-    const float* C = a.Ck + (((size_t)kvh * a.Sk + s) * kCodebook + c0 + chunk * kQtCodes + 8 * warp) * D;
+    if constexpr (SPLIT) {
+      if (chunk < chunks)
+        copy_split<D>(a.books, book0 + chunk * kQtCodes, kQtCodes, sm.c[chunk & 1][0], sm.c[chunk & 1][1], kQtThreads);
+      cp_async_commit();
+      return;
+    }
+    const float* C = a.Ck + (book0 + chunk * kQtCodes + 8 * warp) * D;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float* x = C + k * D + lane * E;
@@ -156,13 +218,20 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int cl = cl0 + 8 * n + 2 * t4 + i;
-        const float x = real ? (acc[2 * q + i] + cross[2 * q + i]) * sm.cs[cl] * qs : 0.f;
+        const float cs = !real ? 0.f : SPLIT ? __ldg(a.books.scale + book0 + chunk * kQtCodes + cl) : sm.cs[cl];
+        const float x = real ? (acc[2 * q + i] + cross[2 * q + i]) * cs * qs : 0.f;
         out[q][((int64_t)(c0 + chunk * kQtCodes + cl) * a.SKP + s) * a.RG] = x;
       }
     }
   };
   for (int chunk = 0; chunk < chunks; ++chunk) {
-    if (real) {
+    constexpr int BUFS = SPLIT ? 2 : 1;
+    const __half *ch = sm.c[chunk % BUFS][0], *cl = sm.c[chunk % BUFS][1];
+    if (SPLIT && real) {
+      cp_async_wait_all();
+      __syncthreads();              // the chunk is there, and the one before has been read
+      load(chunk + 1);
+    } else if (real) {
       __syncthreads();              // the previous chunk has been read
       float part[8], down_of;
 #pragma unroll
@@ -186,15 +255,15 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
         for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
         const int at = tile_at<D>(c, lane * E);
         if constexpr (E == 2) {
-          *reinterpret_cast<uint32_t*>(sm.c[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
-          *reinterpret_cast<uint32_t*>(sm.c[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
+          *reinterpret_cast<uint32_t*>(sm.c[0][0] + at) = *reinterpret_cast<const uint32_t*>(hi);
+          *reinterpret_cast<uint32_t*>(sm.c[0][1] + at) = *reinterpret_cast<const uint32_t*>(lo);
         } else if constexpr (E == 4) {
-          *reinterpret_cast<uint2*>(sm.c[0] + at) = make_uint2(reinterpret_cast<const uint32_t*>(hi)[0], reinterpret_cast<const uint32_t*>(hi)[1]);
-          *reinterpret_cast<uint2*>(sm.c[1] + at) = make_uint2(reinterpret_cast<const uint32_t*>(lo)[0], reinterpret_cast<const uint32_t*>(lo)[1]);
+          *reinterpret_cast<uint2*>(sm.c[0][0] + at) = make_uint2(reinterpret_cast<const uint32_t*>(hi)[0], reinterpret_cast<const uint32_t*>(hi)[1]);
+          *reinterpret_cast<uint2*>(sm.c[0][1] + at) = make_uint2(reinterpret_cast<const uint32_t*>(lo)[0], reinterpret_cast<const uint32_t*>(lo)[1]);
         } else {
           const uint32_t *h4 = reinterpret_cast<const uint32_t*>(hi), *l4 = reinterpret_cast<const uint32_t*>(lo);
-          *reinterpret_cast<uint4*>(sm.c[0] + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-          *reinterpret_cast<uint4*>(sm.c[1] + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+          *reinterpret_cast<uint4*>(sm.c[0][0] + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+          *reinterpret_cast<uint4*>(sm.c[0][1] + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
         }
       }
       __syncthreads();
@@ -206,8 +275,8 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
 #pragma unroll 2
         for (int ks = 0; ks < D / 16; ks += 2) {
           uint32_t bh[4], bl[4];
-          frag_b2<D>(bh, sm.c[0], cl0, ks, lane);
-          frag_b2<D>(bl, sm.c[1], cl0, ks, lane);
+          frag_b2<D>(bh, ch, cl0, ks, lane);
+          frag_b2<D>(bl, cl, cl0, ks, lane);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t ah[4], al[4];
@@ -233,8 +302,8 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
 #pragma unroll
           for (int n = 0; n < 4; n += 2) {
             uint32_t bh[4], bl[4];
-            frag_b<D>(bh, sm.c[0], cl0 + 8 * n, ks, lane);
-            frag_b<D>(bl, sm.c[1], cl0 + 8 * n, ks, lane);
+            frag_b<D>(bh, ch, cl0 + 8 * n, ks, lane);
+            frag_b<D>(bl, cl, cl0 + 8 * n, ks, lane);
             mma16816_add(acc[n], ah, bh[0], bh[1]);
             mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
             mma16816(cross[n], ah, bl[0], bl[1]);

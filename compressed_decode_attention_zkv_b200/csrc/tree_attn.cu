@@ -9,7 +9,8 @@
 // of kTreeRG = 8.  Five kernels per call (programmatic dependent launches):
 //   1. tree_dense_kernel    the dense part (fp16 window and the drafts that the mask names: partial
 //      maximum, sum and output per row); one block computes the partition of the compressed tokens.
-//      tree_tables_kernel   beside it: the key lookup tables of every row (query_tables.cuh).
+//      tree_tables_kernel   beside it: the key lookup tables of every row (query_tables.cuh); with
+//      many rows after tree_split_kernel, which splits the codewords once for them and for 3.
 //   2. tree_scan_kernel     per item and range of tokens: base-2 scores from the tables and the
 //      per-codeword weight histograms W_s[c][row] = sum over the tokens with zv_s = c of
 //      2^(score - ref).  Each (range, item) writes one slot.
@@ -54,6 +55,7 @@ struct TreeArgs {
   int pshift;
   // workspace
   int64_t* pre;            // [B + 1] units of one item of the sequences before b; then the range
+  SplitBooks vbooks;       // of Cv, or null planes
   float *pw, *pm;          // slots: [slot][Sv][256][8] weights, [slot][8] references
   float *dm, *dl, *dout;   // dense part per row: maximum (log2), sum, output [D]
   float *parts;            // [Sv * halves][row][D]
@@ -357,15 +359,27 @@ __global__ void __launch_bounds__(kTreeDenseThreads) tree_dense_kernel(TreeArgs 
   const int64_t blk = (int64_t)blockIdx.x - 1;
   if (blk < 0) tree_partition(a);
   else tree_dense<D>(a, blk, sm);
+  pdl_wait();      // (after a normal launch it returns at once)
 }
 
-// Runs beside the dense part, which it does not read, and completes after it.
+// The key and value codewords split once, 64 a block, for the blocks of the tables and the contraction
 template <int D>
+__global__ void __launch_bounds__(kQtThreads) tree_split_kernel(TreeArgs a) {
+  pdl_trigger();
+  const int64_t keys = (int64_t)a.Hkv * a.Sk * (kCodebook / 64), blk = blockIdx.x;
+  if (blk < keys) split_books_block<D>(a.qt.Ck, a.qt.books, blk * 64);
+  else split_books_block<D>(a.Cv, a.vbooks, (blk - keys) * 64);
+}
+
+// With codewords split before: after that kernel.  Else it runs beside the dense part, which it does
+// not read, and completes after it.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kQtThreads) tree_tables_kernel(TreeArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   pdl_trigger();
-  query_tables_block<D>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D>*>(smraw));
-  pdl_wait();
+  if (SPLIT) pdl_wait();
+  query_tables_block<D, SPLIT>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D, SPLIT>*>(smraw));
+  if (!SPLIT) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -834,7 +848,13 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
   const int64_t group = blockIdx.x / parts;
   const int64_t j = group * 8 + warp;          // (b, rg) of kvh
   pdl_trigger();
-  {
+  if (a.vbooks.hi) {
+    const int64_t row = ((int64_t)kvh * a.Sv + s) * kCodebook + half * kTreeCw;
+    pdl_wait();          // (the planes are this call's)
+    copy_split<D>(a.vbooks, row, kTreeCw, sm.cv[0], sm.cv[1], 256);
+    cp_async_commit();
+    if (tid < kTreeCw) sm.cs[tid] = a.vbooks.scale[row + tid];
+  } else {
     // warp w splits codewords w, w + 8, ...; lane = E dimensions in a row
     const float* C = a.Cv + (((int64_t)kvh * a.Sv + s) * kCodebook + half * kTreeCw) * D + lane * E;
 #pragma unroll 1
@@ -966,6 +986,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
     }
     if (lane == 0) sm.row[warp] = n ? row : -1;
   }
+  cp_async_wait_all();
   __syncthreads();
   const int64_t rows = (int64_t)a.B * a.Hkv * a.RP;
   const int g = lane >> 2, t4 = lane & 3;
@@ -1079,7 +1100,8 @@ static int tree_pad_stages(int S) { return S <= 2 ? S : S <= 4 ? 4 : 8; }
 struct TreePlan {
   int R, RP, NRG, SKP, SVP, grid;
   int64_t items, slots, rows;
-  size_t lut, pre, pw, pm, dm, dl, dout, parts, rm, rl, total;
+  bool split;              // the codewords are split by a kernel of their own
+  size_t lut, pre, pw, pm, dm, dl, dout, parts, rm, rl, kplanes, kscale, vplanes, vscale, total;
 };
 
 static TreePlan tree_plan(const zkv_tree_params* p) {
@@ -1112,6 +1134,15 @@ static TreePlan tree_plan(const zkv_tree_params* p) {
   t.parts = take((size_t)t.rows * p->d * 4 * p->Sv * kTreeHalves);
   t.rm = take((size_t)t.rows * 4);
   t.rl = take((size_t)t.rows * 4 * kTreeHalves);
+  // with four blocks of rows or more per kv head every codeword would be split four times or more
+  t.split = (int64_t)p->B * t.RP > 3 * kQtRows;
+  if (t.split) {
+    const int64_t kr = (int64_t)p->Hkv * p->Sk * kCodebook, vr = (int64_t)p->Hkv * p->Sv * kCodebook;
+    t.kplanes = take(split_books_bytes(kr, p->d));
+    t.kscale = take((size_t)kr * 4);
+    t.vplanes = take(split_books_bytes(vr, p->d));
+    t.vscale = take((size_t)vr * 4);
+  }
   t.total = o;
   return t;
 }
@@ -1171,18 +1202,29 @@ static cudaError_t launch_tree_scan_v(const TreeArgs& a, int SVP, cudaStream_t s
 
 template <int D>
 static int launch_tree(const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
-  const size_t s0 = sizeof(TreeDenseSmem<D>), s1 = sizeof(QtSmem<D>), s3 = sizeof(TreeContractSmem<D>);
-  static_assert(sizeof(QtSmem<D>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax &&
+  const size_t s0 = sizeof(TreeDenseSmem<D>), s1 = sizeof(QtSmem<D, false>), s2 = sizeof(QtSmem<D, true>),
+               s3 = sizeof(TreeContractSmem<D>);
+  static_assert(sizeof(QtSmem<D, true>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax &&
                     sizeof(TreeDenseSmem<D>) <= kTreeSmemMax, "fits");
   if (ensure_smem_limit(tree_dense_kernel<D>, s0) != cudaSuccess ||
-      ensure_smem_limit(tree_tables_kernel<D>, s1) != cudaSuccess ||
+      ensure_smem_limit(tree_tables_kernel<D, false>, s1) != cudaSuccess ||
+      ensure_smem_limit(tree_tables_kernel<D, true>, s2) != cudaSuccess ||
       ensure_smem_limit(tree_contract_kernel<D>, s3) != cudaSuccess)
     return ZKV_ERR_CUDA;
-  const int64_t b0 = 1 + (int64_t)a.B * a.Hkv * ((a.R + kTreeDenseRows - 1) / kTreeDenseRows);
-  tree_dense_kernel<D><<<(unsigned)b0, kTreeDenseThreads, s0, st>>>(a);
-  ZKV_CHECK_LAUNCH();
-  if (launch_pdl(tree_tables_kernel<D>, dim3((unsigned)a.qt.blocks()), dim3(kQtThreads), s1, st, a) != cudaSuccess)
-    return ZKV_ERR_CUDA;
+  const dim3 dense((unsigned)(1 + (int64_t)a.B * a.Hkv * ((a.R + kTreeDenseRows - 1) / kTreeDenseRows)));
+  const dim3 tables((unsigned)a.qt.blocks());
+  if (t.split) {
+    tree_split_kernel<D><<<(unsigned)(a.Hkv * (a.Sk + a.Sv) * (kCodebook / 64)), kQtThreads, 0, st>>>(a);
+    ZKV_CHECK_LAUNCH();
+    if (launch_pdl(tree_tables_kernel<D, true>, tables, dim3(kQtThreads), s2, st, a) != cudaSuccess ||
+        launch_pdl(tree_dense_kernel<D>, dense, dim3(kTreeDenseThreads), s0, st, a) != cudaSuccess)
+      return ZKV_ERR_CUDA;
+  } else {
+    tree_dense_kernel<D><<<dense, kTreeDenseThreads, s0, st>>>(a);
+    ZKV_CHECK_LAUNCH();
+    if (launch_pdl(tree_tables_kernel<D, false>, tables, dim3(kQtThreads), s1, st, a) != cudaSuccess)
+      return ZKV_ERR_CUDA;
+  }
   cudaError_t e;
   switch (t.SKP) {
     case 1: e = launch_tree_scan_v<1>(a, t.SVP, st); break;
@@ -1245,6 +1287,15 @@ extern "C" int zkv_rvq_tree_attn(const zkv_tree_params* p, void* workspace, size
   q.scale_log2 = (float)((double)scale * 1.4426950408889634);
   q.rot = 1.0 / std::sqrt((double)p->d);
   q.lut = reinterpret_cast<float*>(ws + t.lut);
+  if (t.split) {
+    const int64_t kr = (int64_t)p->Hkv * p->Sk * kCodebook, vr = (int64_t)p->Hkv * p->Sv * kCodebook;
+    q.books.hi = reinterpret_cast<__half*>(ws + t.kplanes);
+    q.books.lo = q.books.hi + kr * p->d;
+    q.books.scale = reinterpret_cast<float*>(ws + t.kscale);
+    a.vbooks.hi = reinterpret_cast<__half*>(ws + t.vplanes);
+    a.vbooks.lo = a.vbooks.hi + vr * p->d;
+    a.vbooks.scale = reinterpret_cast<float*>(ws + t.vscale);
+  }
   a.pre = reinterpret_cast<int64_t*>(ws + t.pre);
   a.pw = reinterpret_cast<float*>(ws + t.pw);
   a.pm = reinterpret_cast<float*>(ws + t.pm);

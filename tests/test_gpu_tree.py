@@ -148,6 +148,8 @@ CASES = {
     "two and six": dict(B=1, N=2, Hq=2, Hkv=1, d=64, Sk=2, Sv=6, Tcap=160, comp=[150], W=8, win=[8]),
     "four and two": dict(B=1, N=2, Hq=8, Hkv=1, d=256, Sk=4, Sv=2, Tcap=640, comp=[639], W=40, win=[40]),
     "many rows": dict(B=1, N=67, Hq=8, Hkv=1, d=64, Sk=4, Sv=4, Tcap=640, comp=[600], W=16, win=[16]),
+    "many rows, d 128": dict(B=9, N=9, Hq=6, Hkv=2, d=128, Sk=3, Sv=2, Tcap=320, comp=[300, 0, 5, 320, 200, 128, 127, 1, 77], W=16, win=[16] * 9),
+    "many rows, d 256": dict(B=1, N=50, Hq=4, Hkv=1, d=256, Sk=2, Sv=5, Tcap=320, comp=[311], W=16, win=[16]),
     "longer": dict(B=2, N=2, Hq=4, Hkv=2, d=128, Sk=4, Sv=4, Tcap=20000, comp=[20000, 9001], W=16, win=[16, 16]),
 }
 
