@@ -28,10 +28,21 @@ struct SplitBooks {
 };
 inline size_t split_books_bytes(int64_t rows, int D) { return (size_t)rows * D * 4; }
 
+// Quotients by a divisor that a launch fixes: n / d = n m >> 40 with m = floor(2^40 / d) + 1, exact
+// while n d < 2^40
+struct FixedDivisor {
+  int d;
+  uint64_t m;
+  void set(int x) { d = x; m = (uint64_t(1) << 40) / x + 1; }
+  __device__ __forceinline__ int quotient(int n) const { return (int)(((uint64_t)n * m) >> 40); }
+};
+
 struct QueryTables {
   int B, N, G, Hkv, Sk, SKP, RG;
   int R;          // N * G rows of a (sequence, kv head)
   int RP;         // padded to a multiple of RG
+  FixedDivisor by_rp, by_g, by_rg;      // RP, G and RG
+  void set_divisors() { by_rp.set(RP); by_g.set(G); by_rg.set(RG); }
   const __half* q;
   int64_t q_sb, q_sn, q_sh;
   const int32_t* n_query;   // [B] present queries, or null (N)
@@ -161,7 +172,8 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
     float v[8][E], part[8], down_of;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int j = row0 + warp + 8 * k, b = j / a.RP, rho = j % a.RP, i = rho / a.G, g = rho % a.G;
+      const int j = row0 + warp + 8 * k, b = a.by_rp.quotient(j), rho = j - b * a.RP;
+      const int i = a.by_g.quotient(rho), g = rho - i * a.G;
       const bool there = warp + 8 * k < rows && rho < a.R && i < present_queries(a.n_query, b, a.N);
       const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
 #pragma unroll
@@ -201,27 +213,29 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   const bool few = (int64_t)a.B * a.RP - row0 <= 16;
   const int wr = few ? 0 : warp & 3, cl0 = few ? 8 * warp : 32 * (warp >> 2);
   const int g = lane >> 2, t4 = lane & 3;
-  // this thread's two rows in the tables (null: behind the last)
+  // this thread's two rows in the tables (null: behind the last), at its first codeword
   float* out[2];
+  const int step = a.SKP * a.RG;               // from codeword to codeword
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int j = row0 + 16 * wr + g + 8 * q, b = j / a.RP, rho = j % a.RP;
-    out[q] = b < a.B ? a.lut + (((int64_t)b * a.Hkv + kvh) * (a.RP / a.RG) + rho / a.RG) *
-                                   ((int64_t)kCodebook * a.SKP * a.RG) + rho % a.RG
+    const int j = row0 + 16 * wr + g + 8 * q, b = a.by_rp.quotient(j), rho = j - b * a.RP;
+    const int rg = a.by_rg.quotient(rho);
+    out[q] = b < a.B ? a.lut + (((int64_t)b * a.Hkv + kvh) * (a.RP / a.RG) + rg) * ((int64_t)kCodebook * step) +
+                           (c0 + cl0 + 2 * t4) * step + s * a.RG + (rho - rg * a.RG)
                      : nullptr;
   }
   auto put = [&](int chunk, int n, const float (&acc)[4], const float (&cross)[4]) {
+    const int cl = cl0 + 8 * n + 2 * t4, off = (chunk * kQtCodes + 8 * n) * step;
+    float2 cs = make_float2(0.f, 0.f);
+    if (real)
+      cs = SPLIT ? __ldg(reinterpret_cast<const float2*>(a.books.scale + book0 + chunk * kQtCodes + cl))
+                 : *reinterpret_cast<const float2*>(sm.cs + cl);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (!out[q]) continue;
       const float qs = real ? sm.qs[16 * wr + g + 8 * q] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int cl = cl0 + 8 * n + 2 * t4 + i;
-        const float cs = !real ? 0.f : SPLIT ? __ldg(a.books.scale + book0 + chunk * kQtCodes + cl) : sm.cs[cl];
-        const float x = real ? (acc[2 * q + i] + cross[2 * q + i]) * cs * qs : 0.f;
-        out[q][((int64_t)(c0 + chunk * kQtCodes + cl) * a.SKP + s) * a.RG] = x;
-      }
+      out[q][off] = real ? (acc[2 * q] + cross[2 * q]) * cs.x * qs : 0.f;
+      out[q][off + step] = real ? (acc[2 * q + 1] + cross[2 * q + 1]) * cs.y * qs : 0.f;
     }
   };
   for (int chunk = 0; chunk < chunks; ++chunk) {

@@ -1286,6 +1286,7 @@ extern "C" int zkv_rvq_tree_attn(const zkv_tree_params* p, void* workspace, size
   q.n_query = p->n_draft; q.Ck = p->k_codebooks; q.k_smooth = p->k_smooth;
   q.scale_log2 = (float)((double)scale * 1.4426950408889634);
   q.rot = 1.0 / std::sqrt((double)p->d);
+  q.set_divisors();
   q.lut = reinterpret_cast<float*>(ws + t.lut);
   if (t.split) {
     const int64_t kr = (int64_t)p->Hkv * p->Sk * kCodebook, vr = (int64_t)p->Hkv * p->Sv * kCodebook;

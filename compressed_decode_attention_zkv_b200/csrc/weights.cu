@@ -293,6 +293,7 @@ extern "C" int zkv_rvq_accumulate_weights(const zkv_weights_params* p, void* wor
   q.Ck = p->k_codebooks; q.k_smooth = p->k_smooth;
   q.scale_log2 = (float)((double)scale * 1.4426950408889634);
   q.rot = 1.0 / std::sqrt((double)p->d);
+  q.set_divisors();
   q.lut = reinterpret_cast<float*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = p->d == 64 ? launch_weights_tables<64>(a, st)
