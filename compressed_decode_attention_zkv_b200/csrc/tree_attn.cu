@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kQtThreads) tree_tables_kernel(TreeArgs a) {
 // the lanes of every gather phase and of every counter addition lie in distinct banks, whatever the
 // codes are.
 //
-// Weights.  p = 2^(score - ref) with ref the row's maximum over the first tile.  The block sums p
+// Weights.  p = 2^(score - ref) with ref the row's maximum over the first tokens of the segment.  The block sums p
 // per row over the tile before it adds any (one barrier), so a row's unit can be chosen: a power
 // of two with the first tile's sum at 2^27 .. 2^28 units.  Counters then take u = p / unit, rounded,
 // as exact integers in any order; when the sum of a row could pass 2^32 the counters are folded
@@ -523,6 +523,15 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     b = x;
   }
   int buf = 0;
+  auto load_tables = [&](int64_t item) {      // asynchronous
+    const float* t = a.qt.lut + item * (int64_t)(kCodebook * SKP * kTreeRG);
+    constexpr int Q = SKP * C::KR * 2;    // 16-byte pieces per codeword
+    for (int f = tid; f < kCodebook * Q; f += C::THREADS) {
+      const int c = f / Q, q = f % Q, s = (q >> 1) / C::KR;
+      cp_async16(sm + 256 * c + 16 * q, t + (c * SKP + s) * kTreeRG + 4 * (q & 1));
+    }
+  };
+  bool first = true;
   while (lo < hi) {
     int64_t base = a.pre[b] * items_per_b, units = a.pre[b + 1] - a.pre[b];
     while (units == 0 || lo >= base + units * items_per_b) {
@@ -542,17 +551,17 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
                                   a.Hkv, a.Tcap, a.Sk, a.err);
     const CodeRows vr = code_rows(a.v_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh,
                                   a.Hkv, a.Tcap, a.Sv, a.err);
-    __syncthreads();   // the previous segment's tables are no longer read
-    {
-      const float* t = a.qt.lut + item * (int64_t)(kCodebook * SKP * kTreeRG);
-      constexpr int Q = SKP * C::KR * 2;    // 16-byte pieces per codeword
-      for (int f = tid; f < kCodebook * Q; f += C::THREADS) {
-        const int c = f / Q, q = f % Q, s = (q >> 1) / C::KR;
-        cp_async16(sm + 256 * c + 16 * q, t + (c * SKP + s) * kTreeRG + 4 * (q & 1));
-      }
-      cp_async_wait_all();
-      __syncthreads();
+    // the item of the block's next segment (this one's item ends here if there is one)
+    int64_t next = -1;
+    if (lo + cnt < hi) {
+      next = item + 1;
+      if (in_b + 1 == items_per_b)
+        for (int x = b + 1; a.pre[x + 1] == a.pre[x]; ++x) next += items_per_b;
     }
+    if (first) load_tables(item);
+    first = false;
+    cp_async_wait_all();
+    __syncthreads();
 
     // state of this thread's two rows (the same in every thread that has them)
     float ref[2];                  // (NaN from the first sum on that is not finite: the row is lost)
@@ -677,11 +686,11 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       read_four<SVP, C::VW, decltype(ex)::value>(
           codes + q * C::CODES + 32 * (kTreeTK / 4) * SKP + (32 * k + 4 * h) * S, S, w);
     };
-    // the rows' largest scores of the tile
-    auto tile_max = [&](uint32_t tile, int q, float (&x)[2]) {
+    // the rows' largest scores of the tile's first tokens (groups of 32 per warp)
+    auto tile_max = [&](uint32_t tile, int q, int groups, float (&x)[2]) {
       float2 mx = make_float2(-INFINITY, -INFINITY);
 #pragma unroll 1
-      for (int k = 0; k < kTreeTK / 4 && tile + (k * C::NW + warp) * 32 < tend; ++k) {
+      for (int k = 0; k < groups && tile + (k * C::NW + warp) * 32 < tend; ++k) {
         uint32_t w[4][C::KW];
         key_codes(std::false_type{}, q, k, w);
 #pragma unroll
@@ -744,7 +753,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     fetch(t0, 0);
     cp_async_wait_all();
     __syncwarp();
-    tile_max(t0, 0, ref);
+    tile_max(t0, 0, 1, ref);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (!(fabsf(ref[j]) < 1e30f)) ref[j] = 0.f;
@@ -763,7 +772,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
         const bool up = (sum[0] > 0x1p64f || sum[1] > 0x1p64f) && !again;
         if (!__any_sync(0xffffffffu, up)) break;
         float mx[2], f[2];
-        tile_max(tile, q, mx);
+        tile_max(tile, q, kTreeTK / 4, mx);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const bool raise = sum[j] > 0x1p64f && mx[j] < 1e30f;
@@ -797,6 +806,8 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
         }
         chosen = true;
       }
+      // the segment's last scores have been taken: the next one's tables take their place meanwhile
+      if (next >= 0 && tend - tile <= C::TILE) load_tables(next);
       float mul[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
