@@ -18,13 +18,14 @@
 // one block and written by another.
 // Kernel 2 advances the lengths after all of kernel 1 has read them.
 //
-// Encode.  Per stage the distances ||c||^2 - 2 r . c of the R residuals to all 256 codewords come
-// from the tensor cores (mma_split.cuh), in chunks of CH codewords whose loads are in flight during
-// the chunk before.  Their error is below the row encoder's margin for float32 sums (candidate_margin
-// allows 2.5 d 2^-24 (||r|| + ||c||)^2; the split product is off by less than 2^-21 ||r|| ||c|| and
-// ||c||^2 by d 2^-24 of itself), so the codewords within that margin of the smallest distance hold
-// the nearest one: if there is one it is the choice, else the distances are taken again in float64
-// and ties go to the lowest index, as zkv_rvq_encode decides.
+// Encode.  Per stage approximate distances ||c||^2 - 2 r . c of the R residuals to all 256 codewords
+// come from the tensor cores, residuals and codewords rounded to fp16 (each row scaled by a power of
+// two to a norm of 2^14 .. 2^15, so subnormals do not matter), in chunks of CH codewords whose loads
+// are in flight during the chunk before.  A product of two roundings is off by 2^-10 of itself, so a
+// distance by less than 2^-9 ||r|| ||c||, and the codewords within twice that (and the margin of the
+// float32 row encoder for the rest, candidate_margin) of the smallest distance hold the nearest one.
+// One such codeword is the choice (for Gaussian codewords 15 times of 16); several are told apart by
+// float64 distances, ties to the lowest index, as zkv_rvq_encode decides.
 #include <cfloat>
 #include <cmath>
 
@@ -88,15 +89,15 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
 
 template <int D, int R>
 struct CommitSmem {
-  static constexpr int CH = D == 256 ? 64 : 128;      // codewords per chunk
-  __half c[2][CH * D];                                // codewords, high and low plane
-  __half x[2][R * D];                       // residuals
+  static constexpr int CH = D == 256 ? 64 : 128;      // codewords per chunk (their loads fit in registers)
+  __half c[CH * D];                                   // codewords
+  __half x[R * D];                                    // residuals
   float r[R][D + 4];                        // residuals, float32
   float dist[R][kCodebook + 4];
   float cn[kCodebook];                                // squared norms of the stage's codewords
   float cs[CH];                                       // scales of the chunk's codewords
   float xs[R];                              // scales of the residuals
-  double rn[R];                             // bound of their norms
+  float rn[R];                              // bound of their norms
   uint8_t code[R][kMaxStages];
   int row_b[R];                             // the evictions: sequence (-1: none), k, state
   int64_t row_k[R];
@@ -178,26 +179,22 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
   __syncthreads();
   if (sm.row_b[0] >= 0) {          // rows fill from the front
     if (blockIdx.x > 0) load(0);
-    // residual row r of this warp: v (elements 32 e + lane) to shared memory, float32 and split
+    // residual row r of this warp: v (elements 32 e + lane) to shared memory, float32 and fp16
     auto put_row = [&](int r, const float (&v)[E]) {
-      float ss = 0.f, big = 0.f;
+      float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        ss = fmaf(v[e], v[e], ss);
-        big = fmaxf(big, fabsf(v[e]));
-      }
+      for (int e = 0; e < E; ++e) ss = fmaf(v[e], v[e], ss);
       ss = warp_sum_f32(ss);
-      const int ex = split_exponent(warp_max_f32(big));
+      const int ex = split_exponent(sqrtf(ss));
       const float down = exp2_int(-ex);
       if (lane == 0) {
         sm.xs[r] = exp2_int(ex);
-        sm.rn[r] = sqrt((double)ss) * (1.0 + 1e-4);       // (D + 5 roundings of 2^-24 on ss)
+        sm.rn[r] = sqrtf(ss) * 1.0001f;       // (D + 5 roundings of 2^-24 on ss)
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         sm.r[r][e * 32 + lane] = v[e];
-        const int at = tile_at<D>(r, e * 32 + lane);
-        split(v[e] * down, sm.x[0][at], sm.x[1][at]);
+        sm.x[tile_at<D>(r, e * 32 + lane)] = __float2half_rn(v[e] * down);
       }
     };
 #pragma unroll
@@ -248,49 +245,37 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
         for (int k = 0; k < CW; ++k) {
           const int c = CW * warp + k;
           const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<CW>(k));
-          alignas(16) __half hi[E], lo[E];
+          alignas(16) __half2 y[E / 2];
 #pragma unroll
-          for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
-          const int at = tile_at<D>(c, lane * E);
-          if constexpr (E == 2) {
-            *reinterpret_cast<uint32_t*>(sm.c[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
-            *reinterpret_cast<uint32_t*>(sm.c[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
-          } else if constexpr (E == 4) {
-            *reinterpret_cast<uint2*>(sm.c[0] + at) = *reinterpret_cast<const uint2*>(hi);
-            *reinterpret_cast<uint2*>(sm.c[1] + at) = *reinterpret_cast<const uint2*>(lo);
-          } else {
-            *reinterpret_cast<uint4*>(sm.c[0] + at) = *reinterpret_cast<const uint4*>(hi);
-            *reinterpret_cast<uint4*>(sm.c[1] + at) = *reinterpret_cast<const uint4*>(lo);
-          }
+          for (int e = 0; e < E; e += 2) y[e / 2] = __floats2half2_rn(cw[k][e] * down, cw[k][e + 1] * down);
+          __half* at = sm.c + tile_at<D>(c, lane * E);
+          if constexpr (E == 2) *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(y);
+          else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(y);
+          else *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(y);
         }
         __syncthreads();
         if (s * NC + chunk + 1 < S * NC) load(s * NC + chunk + 1);
         if (8 * warp < CH) {         // 8 codewords per warp
-          float acc[R / 16][4] = {}, cross[R / 16][2][4] = {};
+          float acc[R / 16][2][4] = {};         // (two sums: neither waits for the other)
 #pragma unroll 2
           for (int ks = 0; ks < D / 16; ks += 2) {
-            uint32_t bh[4], bl[4];
-            frag_b2<D>(bh, sm.c[0], 8 * warp, ks, lane);
-            frag_b2<D>(bl, sm.c[1], 8 * warp, ks, lane);
+            uint32_t b[4];
+            frag_b2<D>(b, sm.c, 8 * warp, ks, lane);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int q = 0; q < R / 16; ++q)
 #pragma unroll
-              for (int q = 0; q < R / 16; ++q) {
-                uint32_t ah[4], al[4];
-                frag_a<D>(ah, sm.x[0], 16 * q, ks + i, lane);
-                frag_a<D>(al, sm.x[1], 16 * q, ks + i, lane);
-                mma16816_add(acc[q], ah, bh[2 * i], bh[2 * i + 1]);
-                mma16816(cross[q][0], ah, bl[2 * i], bl[2 * i + 1]);
-                mma16816(cross[q][1], al, bh[2 * i], bh[2 * i + 1]);
+              for (int i = 0; i < 2; ++i) {
+                uint32_t x[4];
+                frag_a<D>(x, sm.x, 16 * q, ks + i, lane);
+                mma16816(acc[q][i], x, b[2 * i], b[2 * i + 1]);
               }
-            }
           }
 #pragma unroll
           for (int q = 0; q < R / 16; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int c = 8 * warp + 2 * t4 + (i & 1), r = 16 * q + g + 8 * (i >> 1);
-              const float dot = (acc[q][i] + (cross[q][0][i] + cross[q][1][i])) * sm.cs[c] * sm.xs[r];
+              const float dot = (acc[q][0][i] + acc[q][1][i]) * sm.cs[c] * sm.xs[r];
               sm.dist[r][chunk * CH + c] = sm.cn[chunk * CH + c] - 2.f * dot;
             }
         }
@@ -311,35 +296,68 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
           dmin = fminf(dmin, d[j]);
         }
         dmin = warp_min_f32(dmin);
-        const double thr = (double)dmin + candidate_margin(sm.rn[r], cmax, D);
+        // candidate_margin's bound and 2^-8 ||r|| ||c|| (and a little for the sums of the products) for
+        // the fp16 roundings, in float32 arithmetic: 0.1 % and the additions' roundings more
+        constexpr float K = 2.5f * (D + 3) / 16777216.f;
+        const float bn = sqrtf(cmax) * 1.0001f, both = sm.rn[r] + bn;
+        const float thr = dmin + (K * both * both + 0.0040f * sm.rn[r] * bn) * 1.001f + 2.4e-7f * fabsf(dmin) + 1e-30f;
         unsigned cand[8];
         int count = 0, z = kCodebook;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          cand[j] = __ballot_sync(0xffffffffu, (double)d[j] <= thr);
+          cand[j] = __ballot_sync(0xffffffffu, d[j] <= thr);
           count += __popc(cand[j]);
           if (cand[j] && z == kCodebook) z = 32 * j + __ffs(cand[j]) - 1;
         }
         const float* C = CB + (size_t)s * kCodebook * D;
-        if (count > 1) {           // several within the margin: float64 distances
+        if (count > 1) {           // several within the margin: float64 distances, four at a time
           double best = DBL_MAX;
           z = kCodebook;
+          int c[4], have = 0;
+          auto weigh = [&]() {
+            double a[4];
+            float y[4][E];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            for (unsigned x = cand[j]; x; x &= x - 1u) {
-              const int c = 32 * j + __ffs(x) - 1;
-              double a = 0.0;
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int e = 0; e < E; ++e) y[u][e] = __ldg(C + (size_t)c[u < have ? u : 0] * D + e * 32 + lane);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              a[u] = 0.0;
 #pragma unroll
               for (int e = 0; e < E; ++e) {
-                const double df = (double)sm.r[r][e * 32 + lane] - (double)__ldg(C + (size_t)c * D + e * 32 + lane);
-                a = fma(df, df, a);
-              }
-              a = warp_sum_f64(a);
-              if (a < best) {      // (ascending indices: ties keep the lowest)
-                best = a;
-                z = c;
+                const double df = (double)sm.r[r][e * 32 + lane] - (double)y[u][e];
+                a[u] = fma(df, df, a[u]);
               }
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) a[u] += __shfl_xor_sync(0xffffffffu, a[u], o);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (u < have && a[u] < best) {      // (ascending indices: ties keep the lowest)
+                best = a[u];
+                z = c[u];
+              }
+            have = 0;
+          };
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            unsigned x = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i == j) x = cand[i];
+            for (; x; x &= x - 1u) {
+              const int cx = 32 * j + __ffs(x) - 1;
+              if (have == 0) c[0] = cx;
+              else if (have == 1) c[1] = cx;
+              else if (have == 2) c[2] = cx;
+              else c[3] = cx;
+              if (++have == 4) weigh();
+            }
+          }
+          if (have) weigh();
         }
         // a row that is not finite matches no candidate: code 0
         if (z >= kCodebook) z = 0;
