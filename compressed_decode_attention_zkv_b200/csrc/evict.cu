@@ -39,6 +39,7 @@ struct EvictArgs {
   uint8_t *k_out, *v_out;
   float* acc_out;
   int32_t* kept;
+  int32_t* len_out;                 // null: a kernel after this one writes it (it is comp_len)
   int32_t* err;
   const int32_t *table, *table_out;
   int64_t max_pages, n_pages, max_pages_out, n_pages_out;
@@ -54,7 +55,7 @@ __device__ __forceinline__ uint32_t total_key(float x) {
 }
 
 struct EvictSmem {
-  uint32_t hist[kEvBins];
+  uint32_t hist[2][kEvBins];        // passes take turns
   uint32_t ws[2][kEvWarps];
   uint32_t digit, before;           // chosen digit; keys of the cluster above it
   alignas(8) uint32_t count[2];     // this CTA's larger and equal keys
@@ -126,11 +127,16 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   const int64_t pair = blockIdx.x / C;
   const int b = (int)(pair / a.Hkv), kvh = (int)(pair % a.Hkv);
   pdl_trigger();
+  auto cluster_sync = [&]() {
+    if (C > 1) cluster.sync();
+    else __syncthreads();
+  };
   int64_t n = a.comp_len[b];
   if (n < 0 || n > a.Tcap) {
     if (tid == 0 && rank == 0) set_error(a.err, ZKV_DEVERR_COMP_LEN);
     n = n < 0 ? 0 : a.Tcap;
   }
+  if (a.len_out && kvh == 0 && rank == 0 && tid == 0) a.len_out[b] = (int32_t)(n < a.keep ? n : a.keep);
   const bool all_kept = n <= a.keep;
   const int m = (int)(all_kept ? n : a.keep);
   const int old = (int)(all_kept ? 0 : n - a.recent);       // tokens before the newest
@@ -150,13 +156,15 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int nb = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < kEvBins; i += kEvThreads) sm.hist[i] = 0u;
+      // (its last readers, two passes ago, came to the barrier of the pass between)
+      uint32_t* hist = sm.hist[pass & 1];
+      for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0u;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < KPT; ++k)
         if (first + 32 * k < old && (keys[k] & mask) == prefix)
-          atomicAdd(&sm.hist[(keys[k] >> shift) & (nb - 1)], 1u);
-      cluster.sync();
+          atomicAdd(&hist[(keys[k] >> shift) & (nb - 1)], 1u);
+      cluster_sync();
       // the cluster's counts from the highest digit down: thread i has digits 2 i and 2 i + 1
       static_assert(kEvBins == 2 * kEvThreads, "two digits per thread");
       const int d0 = nb - 2 - 2 * tid;
@@ -165,7 +173,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
         uint2 x[kEvMaxCl];                     // (all reads in flight)
 #pragma unroll
         for (int c = 0; c < kEvMaxCl; ++c)
-          x[c] = c < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&sm.hist[0], c) + d0)
+          x[c] = c < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, c) + d0)
                        : make_uint2(0u, 0u);
 #pragma unroll
         for (int c = 0; c < kEvMaxCl; ++c) h.x += x[c].x, h.y += x[c].y;
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
         sm.digit = (uint32_t)(d0 + (upper ? 1 : 0));
         sm.before = before + (upper ? 0u : h.y);
       }
-      cluster.sync();          // (every CTA has read the counts, and this block its digit)
+      __syncthreads();         // (the digit is there)
       prefix |= sm.digit << shift;
       mask |= (uint32_t)(nb - 1) << shift;
       want -= sm.before;
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
     sm.count[0] = ag;
     sm.count[1] = ae;
   }
-  cluster.sync();
+  cluster_sync();
   uint32_t cg0 = 0, ce0 = 0;   // of the CTAs before this one
 #pragma unroll
   for (int r = 0; r < kEvMaxCl - 1; ++r)
@@ -265,31 +273,53 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   };
   auto total = [&](uint32_t t) { return acc[t]; };
   if (!a.in_place) {
-    auto move = [&](const CodeRows& rows, uint8_t* out, int S) {
-      auto words = [&](auto word) {            // contiguous rows of one machine word each
-        using W = decltype(word);
-        const W* from = reinterpret_cast<const W*>(rows.base);
-        W* to = reinterpret_cast<W*>(out + ((int64_t)pair * a.Tout + base) * S);
-        each([&](uint32_t t) { return from[t]; }, [&](uint32_t i, W x) { to[i] = x; });
-      };
-      const bool plain = !a.table && !a.table_out;
-      if (plain && S == 4) return words(uint32_t());
-      if (plain && S == 2) return words(uint16_t());
-      if (plain && S == 1) return words(uint8_t());
-      if (plain && S == 8) return words(uint2());
-      each([&](uint32_t t) {
-             uint32_t w[2];
-             load_codes<8, false>(rows, t, S, w);
-             return make_uint2(w[0], w[1]);
-           },
-           [&](uint32_t i, uint2 x) {
-             const uint32_t w[2] = {x.x, x.y};
-             store_codes(out_row(out, a, b, kvh, base + i, S), S, w);
-           });
+    // contiguous rows of one machine word each: f(a value of that word's type)
+    auto with_word = [](int S, auto f) {
+      if (S == 4) f(uint32_t());
+      else if (S == 2) f(uint16_t());
+      else if (S == 1) f(uint8_t());
+      else f(uint2());
     };
-    move(kr, a.k_out, a.Sk);
-    move(vr, a.v_out, a.Sv);
-    each(total, [&](uint32_t i, float x) { acc_out[base + i] = x; });
+    const bool words = !a.table && !a.table_out && !(a.Sk & (a.Sk - 1)) && !(a.Sv & (a.Sv - 1));
+    if (words) {
+      with_word(a.Sk, [&](auto k_word) {
+        with_word(a.Sv, [&](auto v_word) {
+          using K = decltype(k_word);
+          using V = decltype(v_word);
+          struct Row {
+            K k;
+            V v;
+            float x;
+          };
+          const K* k_from = reinterpret_cast<const K*>(kr.base);
+          const V* v_from = reinterpret_cast<const V*>(vr.base);
+          const int64_t to = pair * a.Tout + base;
+          K* k_to = reinterpret_cast<K*>(a.k_out) + to;
+          V* v_to = reinterpret_cast<V*>(a.v_out) + to;
+          each([&](uint32_t t) { return Row{k_from[t], v_from[t], acc[t]}; },
+               [&](uint32_t i, const Row& r) {
+                 k_to[i] = r.k;
+                 v_to[i] = r.v;
+                 acc_out[base + i] = r.x;
+               });
+        });
+      });
+    } else {
+      auto move = [&](const CodeRows& rows, uint8_t* out, int S) {
+        each([&](uint32_t t) {
+               uint32_t w[2];
+               load_codes<8, false>(rows, t, S, w);
+               return make_uint2(w[0], w[1]);
+             },
+             [&](uint32_t i, uint2 x) {
+               const uint32_t w[2] = {x.x, x.y};
+               store_codes(out_row(out, a, b, kvh, base + i, S), S, w);
+             });
+      };
+      move(kr, a.k_out, a.Sk);
+      move(vr, a.v_out, a.Sv);
+      each(total, [&](uint32_t i, float x) { acc_out[base + i] = x; });
+    }
   } else {
     // four bytes of every kept row at a time: K, V (two turns each for more than four stages), totals
     const int tk = (a.Sk + 3) / 4, tv = (a.Sv + 3) / 4;
@@ -309,7 +339,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
              },
              [&](uint32_t i, uint32_t x) { list[i] = x; });
       }
-      cluster.sync();          // every source of this turn has been read
+      cluster_sync();          // every source of this turn has been read
       for (uint32_t i = tid; i < kept_here; i += kEvThreads) {
         const int64_t j = base + i;
         const uint32_t w = list[i];
@@ -337,7 +367,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   for (int64_t j = m + rank * kEvThreads + tid; j < zero_to; j += all) acc_out[j] = 0.f;
   if (a.kept)
     for (int64_t j = m + rank * kEvThreads + tid; j < a.keep; j += all) a.kept[pair * a.keep + j] = -1;
-  cluster.sync();              // no CTA leaves while another may read its shared memory
+  cluster_sync();              // no CTA leaves while another may read its shared memory
 }
 
 // after every CTA has read comp_len (len_out may be the same array)
@@ -411,6 +441,8 @@ extern "C" int zkv_rvq_evict(const zkv_evict_params* p, void* stream) {
   a.pshift = p->block_table ? log2_pow2(p->page_tokens) : 0;
   a.pshift_out = p->block_table_out ? log2_pow2(p->page_tokens_out) : 0;
   a.in_place = codes_in_place || p->acc_out == p->acc;
+  // (every block reads comp_len: where len_out is that array, a second kernel writes it)
+  a.len_out = p->len_out == p->comp_len ? nullptr : p->len_out;
   // CTAs per cluster: what the capacity needs at 32768 tokens each, then more while there are SMs for
   // them and each keeps 4096 tokens
   const int64_t pairs = (int64_t)p->B * p->Hkv;
@@ -424,6 +456,7 @@ extern "C" int zkv_rvq_evict(const zkv_evict_params* p, void* stream) {
                         : per <= kEvThreads * 16 ? launch_evict<16>(a, C, st)
                                                  : launch_evict<32>(a, C, st);
   if (e != cudaSuccess) return ZKV_ERR_CUDA;
+  if (a.len_out) return ZKV_OK;
   if (launch_pdl(evict_lengths_kernel, dim3((p->B + 127) / 128), dim3(128), 0, st, (int)p->B, p->Tcap, p->keep,
                  p->comp_len, p->len_out) != cudaSuccess)
     return ZKV_ERR_CUDA;
