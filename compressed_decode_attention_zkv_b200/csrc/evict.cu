@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t total_key(float x) {
 struct EvictSmem {
   uint32_t hist[2][kEvBins];        // passes take turns
   uint32_t ws[2][kEvWarps];
-  uint32_t digit, before;           // chosen digit; keys of the cluster above it
+  uint32_t digit, before, found;    // chosen digit; keys of the cluster above it, and with it
   alignas(8) uint32_t count[2];     // this CTA's larger and equal keys
 };
 
@@ -146,10 +146,15 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
 
   uint32_t threshold = 0u;
   int equal = 0;               // tokens with that key that are kept
+  bool ties = false;           // more have it
   uint32_t keys[KPT];
   if (heavy > 0) {
+    // (no branch: all loads are in flight together; old > 0 here)
+    float x[KPT];
 #pragma unroll
-    for (int k = 0; k < KPT; ++k) keys[k] = first + 32 * k < old ? total_key(acc[first + 32 * k]) : 0u;
+    for (int k = 0; k < KPT; ++k) x[k] = acc[min(first + 32 * k, old - 1)];
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) keys[k] = total_key(x[k]);
     uint32_t prefix = 0u, mask = 0u;
     uint32_t want = heavy;     // rank of the sought key among those that match the prefix
 #pragma unroll 1
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
         const bool upper = want <= before + h.y;
         sm.digit = (uint32_t)(d0 + (upper ? 1 : 0));
         sm.before = before + (upper ? 0u : h.y);
+        sm.found = upper ? h.y : h.x;
       }
       __syncthreads();         // (the digit is there)
       prefix |= sm.digit << shift;
@@ -194,17 +200,33 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
     }
     threshold = prefix;
     equal = (int)want;
+    ties = sm.found > want;
   }
   // flags: group k of the warp is word warp * KPT + k; its kept-for-certain and equal tokens
   static_assert(KPT <= 32, "one lane per word");
   uint32_t gt_of = 0u, eq_of = 0u;                          // word lane of the warp
+  if (heavy == 0) {
 #pragma unroll
-  for (int k = 0; k < KPT; ++k) {
-    const int t = first + 32 * k;
-    const bool is_old = t < old;
-    const unsigned gt = __ballot_sync(0xffffffffu, t < n && (!is_old || (heavy > 0 && keys[k] > threshold)));
-    const unsigned eq = __ballot_sync(0xffffffffu, is_old && heavy > 0 && keys[k] == threshold);
-    if (lane == k) gt_of = gt, eq_of = eq;
+    for (int k = 0; k < KPT; ++k) {
+      const int t = first + 32 * k;
+      const unsigned gt = __ballot_sync(0xffffffffu, (t >= old) & (t < n));
+      if (lane == k) gt_of = gt;
+    }
+  } else {
+    const int oldest = old - first, end = (int)n - first;      // of this lane's tokens: 32 k
+    const uint32_t from = ties ? threshold + 1u : threshold;   // (an infinity's key is 2^32 - 2^23)
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+      const bool is_old = 32 * k < oldest;
+      const unsigned gt = __ballot_sync(0xffffffffu, ((!is_old) | (keys[k] >= from)) & (32 * k < end));
+      if (lane == k) gt_of = gt;
+    }
+    if (ties)
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const unsigned eq = __ballot_sync(0xffffffffu, (32 * k < oldest) & (keys[k] == threshold));
+        if (lane == k) eq_of = eq;
+      }
   }
   // (gt, eq) before each word: of the warp, the CTA and the cluster
   const uint32_t g = warp_scan(__popc(gt_of), lane), e = warp_scan(__popc(eq_of), lane);

@@ -170,15 +170,31 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
     // the block's rows, rotated (float32 transform): warp w takes rows w, w + 8, ...
     const int rows = a.B * a.RP - row0;          // rows from here on
     float v[8][E], part[8], down_of;
+    // (rows that are not there read the first one: all loads are in flight together)
+    bool there[8];
+    int i[8], g[8], b[8], present[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int j = row0 + warp + 8 * k, b = a.by_rp.quotient(j), rho = j - b * a.RP;
-      const int i = a.by_g.quotient(rho), g = rho - i * a.G;
-      const bool there = warp + 8 * k < rows && rho < a.R && i < present_queries(a.n_query, b, a.N);
-      const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = there ? __half2float(qr[e * 32]) : 0.f;
+      const int j = row0 + warp + 8 * k;
+      b[k] = a.by_rp.quotient(j);
+      const int rho = j - b[k] * a.RP;
+      i[k] = a.by_g.quotient(rho);
+      g[k] = rho - i[k] * a.G;
+      there[k] = warp + 8 * k < rows && rho < a.R;
+      if (!there[k]) b[k] = i[k] = g[k] = 0;
+      present[k] = a.n_query ? a.n_query[b[k]] : a.N;
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const __half* qr = a.q + b[k] * a.q_sb + i[k] * a.q_sn + ((int64_t)kvh * a.G + g[k]) * a.q_sh + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = __half2float(qr[e * 32]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (!there[k] || i[k] >= present[k])
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       part[k] = 0.f;

@@ -511,16 +511,14 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     if (tid == 0) set_error(a.err, ZKV_DEVERR_SMEM);
     return;
   }
-  // the sequence of the first unit: the last b with pre[b] * items_per_b <= lo
-  int b = 0;
-  {
-    int x = 0, y = a.B;
-    while (y - x > 1) {
-      const int m = (x + y) / 2;
-      if (a.pre[m] * items_per_b <= lo) x = m;
-      else y = m;
-    }
-    b = x;
+  // the sequence of the first unit: the last b with pre[b] * items_per_b <= lo (32 at a time: the
+  // prefix sums do not fall)
+  int b = -1;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const unsigned below =
+        __ballot_sync(0xffffffffu, b0 + lane < a.B && a.pre[min(b0 + lane, a.B - 1)] * items_per_b <= lo);
+    b += __popc(below);
+    if (below != 0xffffffffu) break;
   }
   int buf = 0;
   auto load_tables = [&](int64_t item) {      // asynchronous
@@ -925,6 +923,7 @@ __global__ void __launch_bounds__(256, D <= 128 ? 2 : 1) tree_contract_kernel(Tr
     bool nan[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) m[q] = -INFINITY, nan[q] = false;
+#pragma unroll 4
     for (int64_t k = 0; k < n; ++k) {
       const float4 x = *reinterpret_cast<const float4*>(a.pm + (slot0 + k) * kTreeRG + r4);
       m[0] = fmaxf(m[0], x.x); m[1] = fmaxf(m[1], x.y);

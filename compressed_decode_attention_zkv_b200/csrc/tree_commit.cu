@@ -53,10 +53,11 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
     err = ZKV_DEVERR_DRAFT;
     return false;
   }
-  for (int64_t i = 0; i < s.n; i += 8) {
-    int32_t x[8];                    // (eight loads in flight)
+  const int32_t* path = p.path + b * p.M;
+  for (int i = 0; i < (int)s.n; i += 8) {
+    int32_t x[8];                    // (eight loads in flight, the last entry again behind it)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = i + q < s.n ? p.path[b * p.M + i + q] : 0;
+    for (int q = 0; q < 8; ++q) x[q] = path[min(i + q, (int)s.n - 1)];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       if (x[q] < 0 || x[q] >= p.N) err = ZKV_DEVERR_DRAFT;
