@@ -11,8 +11,8 @@
 // (mma_split.cuh).  Block = 64 rows of one kv head (rows of several sequences side by side: they
 // share the codewords) x one stage; it rotates its rows once and takes the codewords in chunks of
 // 64, the next chunk's loads in flight during a chunk's products.  With few blocks the chunks of a
-// stage are shared out over 2 or 4 blocks.  The codewords are split in the block, or, where many
-// blocks would repeat that, come split from a kernel before (SplitBooks).
+// stage are shared out over 2 or 4 blocks.  Every block splits the codewords that it uses; where many
+// would repeat that, the tree attention takes tree_tables_tc.cuh and codewords split before (SplitBooks).
 #pragma once
 
 #include "mma_split.cuh"
@@ -118,16 +118,16 @@ __device__ __forceinline__ void split_books_block(const float* src, const SplitB
   }
 }
 
-template <int D, bool SPLIT>
+template <int D>
 struct QtSmem {
   __half q[2][kQtRows * D];       // rotated queries: high and low plane
-  __half c[SPLIT ? 2 : 1][2][kQtCodes * D];      // codewords (split before: two chunks in flight)
+  __half c[2][kQtCodes * D];      // codewords
   float qs[kQtRows];              // their scales (softmax scale included)
   float cs[kQtCodes];
 };
 
-template <int D, bool SPLIT>
-__device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t blk, QtSmem<D, SPLIT>& sm) {
+template <int D>
+__device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t blk, QtSmem<D>& sm) {
   constexpr int E = D / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int shares = a.shares(), chunks = kCodebook / kQtCodes / shares;
@@ -143,12 +143,6 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   float cw[8][E];
   const int64_t book0 = ((int64_t)kvh * a.Sk + s) * kCodebook + c0;      // the block's first codeword
   auto load = [&](int chunk) {
-    if constexpr (SPLIT) {
-      if (chunk < chunks)
-        copy_split<D>(a.books, book0 + chunk * kQtCodes, kQtCodes, sm.c[chunk & 1][0], sm.c[chunk & 1][1], kQtThreads);
-      cp_async_commit();
-      return;
-    }
     const float* C = a.Ck + (book0 + chunk * kQtCodes + 8 * warp) * D;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -243,9 +237,7 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
   auto put = [&](int chunk, int n, const float (&acc)[4], const float (&cross)[4]) {
     const int cl = cl0 + 8 * n + 2 * t4, off = (chunk * kQtCodes + 8 * n) * step;
     float2 cs = make_float2(0.f, 0.f);
-    if (real)
-      cs = SPLIT ? __ldg(reinterpret_cast<const float2*>(a.books.scale + book0 + chunk * kQtCodes + cl))
-                 : *reinterpret_cast<const float2*>(sm.cs + cl);
+    if (real) cs = *reinterpret_cast<const float2*>(sm.cs + cl);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (!out[q]) continue;
@@ -255,13 +247,7 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
     }
   };
   for (int chunk = 0; chunk < chunks; ++chunk) {
-    constexpr int BUFS = SPLIT ? 2 : 1;
-    const __half *ch = sm.c[chunk % BUFS][0], *cl = sm.c[chunk % BUFS][1];
-    if (SPLIT && real) {
-      cp_async_wait_all();
-      __syncthreads();              // the chunk is there, and the one before has been read
-      load(chunk + 1);
-    } else if (real) {
+    if (real) {
       __syncthreads();              // the previous chunk has been read
       float part[8], down_of;
 #pragma unroll
@@ -285,15 +271,15 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
         for (int e = 0; e < E; ++e) split(cw[k][e] * down, hi[e], lo[e]);
         const int at = tile_at<D>(c, lane * E);
         if constexpr (E == 2) {
-          *reinterpret_cast<uint32_t*>(sm.c[0][0] + at) = *reinterpret_cast<const uint32_t*>(hi);
-          *reinterpret_cast<uint32_t*>(sm.c[0][1] + at) = *reinterpret_cast<const uint32_t*>(lo);
+          *reinterpret_cast<uint32_t*>(sm.c[0] + at) = *reinterpret_cast<const uint32_t*>(hi);
+          *reinterpret_cast<uint32_t*>(sm.c[1] + at) = *reinterpret_cast<const uint32_t*>(lo);
         } else if constexpr (E == 4) {
-          *reinterpret_cast<uint2*>(sm.c[0][0] + at) = make_uint2(reinterpret_cast<const uint32_t*>(hi)[0], reinterpret_cast<const uint32_t*>(hi)[1]);
-          *reinterpret_cast<uint2*>(sm.c[0][1] + at) = make_uint2(reinterpret_cast<const uint32_t*>(lo)[0], reinterpret_cast<const uint32_t*>(lo)[1]);
+          *reinterpret_cast<uint2*>(sm.c[0] + at) = make_uint2(reinterpret_cast<const uint32_t*>(hi)[0], reinterpret_cast<const uint32_t*>(hi)[1]);
+          *reinterpret_cast<uint2*>(sm.c[1] + at) = make_uint2(reinterpret_cast<const uint32_t*>(lo)[0], reinterpret_cast<const uint32_t*>(lo)[1]);
         } else {
           const uint32_t *h4 = reinterpret_cast<const uint32_t*>(hi), *l4 = reinterpret_cast<const uint32_t*>(lo);
-          *reinterpret_cast<uint4*>(sm.c[0][0] + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-          *reinterpret_cast<uint4*>(sm.c[0][1] + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+          *reinterpret_cast<uint4*>(sm.c[0] + at) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+          *reinterpret_cast<uint4*>(sm.c[1] + at) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
         }
       }
       __syncthreads();
@@ -305,8 +291,8 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
 #pragma unroll 2
         for (int ks = 0; ks < D / 16; ks += 2) {
           uint32_t bh[4], bl[4];
-          frag_b2<D>(bh, ch, cl0, ks, lane);
-          frag_b2<D>(bl, cl, cl0, ks, lane);
+          frag_b2<D>(bh, sm.c[0], cl0, ks, lane);
+          frag_b2<D>(bl, sm.c[1], cl0, ks, lane);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t ah[4], al[4];
@@ -332,8 +318,8 @@ __device__ __forceinline__ void query_tables_block(const QueryTables& a, int64_t
 #pragma unroll
           for (int n = 0; n < 4; n += 2) {
             uint32_t bh[4], bl[4];
-            frag_b<D>(bh, ch, cl0 + 8 * n, ks, lane);
-            frag_b<D>(bl, cl, cl0 + 8 * n, ks, lane);
+            frag_b<D>(bh, sm.c[0], cl0 + 8 * n, ks, lane);
+            frag_b<D>(bl, sm.c[1], cl0 + 8 * n, ks, lane);
             mma16816_add(acc[n], ah, bh[0], bh[1]);
             mma16816_add(acc[n + 1], ah, bh[2], bh[3]);
             mma16816(cross[n], ah, bl[0], bl[1]);

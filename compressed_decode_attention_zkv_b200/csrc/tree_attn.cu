@@ -18,6 +18,7 @@
 //      one part per (stage, half of the codewords).
 //   4. tree_finish_kernel   sums the parts, rotates back, joins the dense part by log-sum-exp.
 #include "query_tables.cuh"
+#include "tree_tables_tc.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -371,15 +372,22 @@ __global__ void __launch_bounds__(kQtThreads) tree_split_kernel(TreeArgs a) {
   else split_books_block<D>(a.Cv, a.vbooks, (blk - keys) * 64);
 }
 
-// With codewords split before: after that kernel.  Else it runs beside the dense part, which it does
-// not read, and completes after it.
-template <int D, bool SPLIT>
+// Few rows: runs beside the dense part, which it does not read, and completes after it
+template <int D>
 __global__ void __launch_bounds__(kQtThreads) tree_tables_kernel(TreeArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   pdl_trigger();
-  if (SPLIT) pdl_wait();
-  query_tables_block<D, SPLIT>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D, SPLIT>*>(smraw));
-  if (!SPLIT) pdl_wait();
+  query_tables_block<D>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D>*>(smraw));
+  pdl_wait();
+}
+
+// Many rows, after the split kernel
+template <int D>
+__global__ void __launch_bounds__(kTtThreads, 1) tree_tables_tc_kernel(TreeArgs a, int shares) {
+  extern __shared__ __align__(1024) unsigned char smraw[];
+  pdl_trigger();
+  TtSmem<D>& sm = *reinterpret_cast<TtSmem<D>*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
+  tree_tables_tc<D>(a.qt, blockIdx.x, shares, sm, a.err);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1212,27 +1220,36 @@ static cudaError_t launch_tree_scan_v(const TreeArgs& a, int SVP, cudaStream_t s
 
 template <int D>
 static int launch_tree(const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
-  const size_t s0 = sizeof(TreeDenseSmem<D>), s1 = sizeof(QtSmem<D, false>), s2 = sizeof(QtSmem<D, true>),
+  const size_t s0 = sizeof(TreeDenseSmem<D>), s1 = sizeof(QtSmem<D>), s2 = tt_smem_bytes<D>(),
                s3 = sizeof(TreeContractSmem<D>);
-  static_assert(sizeof(QtSmem<D, true>) <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax &&
-                    sizeof(TreeDenseSmem<D>) <= kTreeSmemMax, "fits");
+  static_assert(tt_smem_bytes<D>() <= kTreeSmemMax && sizeof(TreeContractSmem<D>) <= kTreeSmemMax &&
+                    sizeof(TreeDenseSmem<D>) <= kTreeSmemMax && sizeof(QtSmem<D>) <= kTreeSmemMax, "fits");
   if (ensure_smem_limit(tree_dense_kernel<D>, s0) != cudaSuccess ||
-      ensure_smem_limit(tree_tables_kernel<D, false>, s1) != cudaSuccess ||
-      ensure_smem_limit(tree_tables_kernel<D, true>, s2) != cudaSuccess ||
+      ensure_smem_limit(tree_tables_kernel<D>, s1) != cudaSuccess ||
+      ensure_smem_limit(tree_tables_tc_kernel<D>, s2) != cudaSuccess ||
       ensure_smem_limit(tree_contract_kernel<D>, s3) != cudaSuccess)
     return ZKV_ERR_CUDA;
   const dim3 dense((unsigned)(1 + (int64_t)a.B * a.Hkv * ((a.R + kTreeDenseRows - 1) / kTreeDenseRows)));
-  const dim3 tables((unsigned)a.qt.blocks());
   if (t.split) {
     tree_split_kernel<D><<<(unsigned)(a.Hkv * (a.Sk + a.Sv) * (kCodebook / 64)), kQtThreads, 0, st>>>(a);
     ZKV_CHECK_LAUNCH();
-    if (launch_pdl(tree_tables_kernel<D, true>, tables, dim3(kQtThreads), s2, st, a) != cudaSuccess ||
+    // blocks that share a tile's stages: the least time over waves of one block per SM, a block's set-up
+    // taken as two thirds of a stage
+    const int64_t tiles = ((int64_t)a.B * a.RP + kTtRows - 1) / kTtRows * a.Hkv;
+    int shares = 1;
+    int64_t best = INT64_MAX;
+    for (int x = 1; x <= a.Sk; ++x) {
+      const int64_t cost = (tiles * x + 147) / 148 * (2 + 3 * ((a.Sk + x - 1) / x));
+      if (cost < best) best = cost, shares = x;
+    }
+    if (launch_pdl(tree_tables_tc_kernel<D>, dim3((unsigned)(tiles * shares)), dim3(kTtThreads), s2, st, a, shares) !=
+            cudaSuccess ||
         launch_pdl(tree_dense_kernel<D>, dense, dim3(kTreeDenseThreads), s0, st, a) != cudaSuccess)
       return ZKV_ERR_CUDA;
   } else {
     tree_dense_kernel<D><<<dense, kTreeDenseThreads, s0, st>>>(a);
     ZKV_CHECK_LAUNCH();
-    if (launch_pdl(tree_tables_kernel<D, false>, tables, dim3(kQtThreads), s1, st, a) != cudaSuccess)
+    if (launch_pdl(tree_tables_kernel<D>, dim3((unsigned)a.qt.blocks()), dim3(kQtThreads), s1, st, a) != cudaSuccess)
       return ZKV_ERR_CUDA;
   }
   cudaError_t e;

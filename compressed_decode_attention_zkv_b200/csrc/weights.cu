@@ -45,7 +45,7 @@ template <int D>
 __global__ void __launch_bounds__(kQtThreads) weights_tables_kernel(WeightArgs a) {
   extern __shared__ __align__(16) unsigned char smraw[];
   pdl_trigger();
-  query_tables_block<D, false>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D, false>*>(smraw));
+  query_tables_block<D>(a.qt, blockIdx.x, *reinterpret_cast<QtSmem<D>*>(smraw));
 }
 
 // RG rows per group (4 or 8), SKP padded stages; a codeword's row: [stage][half][copy] 16-byte pieces
@@ -244,9 +244,9 @@ static cudaError_t launch_weights_scan(const WeightArgs& a, dim3 grid, cudaStrea
 
 template <int D>
 static cudaError_t launch_weights_tables(const WeightArgs& a, cudaStream_t st) {
-  const cudaError_t e = ensure_smem_limit(weights_tables_kernel<D>, sizeof(QtSmem<D, false>));
+  const cudaError_t e = ensure_smem_limit(weights_tables_kernel<D>, sizeof(QtSmem<D>));
   if (e != cudaSuccess) return e;
-  weights_tables_kernel<D><<<(unsigned)a.qt.blocks(), kQtThreads, sizeof(QtSmem<D, false>), st>>>(a);
+  weights_tables_kernel<D><<<(unsigned)a.qt.blocks(), kQtThreads, sizeof(QtSmem<D>), st>>>(a);
   return cudaGetLastError();
 }
 
