@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kQtThreads) tree_tables_kernel(TreeArgs a) {
 // Many rows, after the split kernel
 template <int D>
 __global__ void __launch_bounds__(kTtThreads, 1) tree_tables_tc_kernel(TreeArgs a, int shares) {
-  extern __shared__ __align__(1024) unsigned char smraw[];
+  extern __shared__ __align__(16) unsigned char smraw[];
   pdl_trigger();
   TtSmem<D>& sm = *reinterpret_cast<TtSmem<D>*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   tree_tables_tc<D>(a.qt, blockIdx.x, shares, sm, a.err);
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
     __syncthreads();
 
     // state of this thread's two rows (the same in every thread that has them)
-    float ref[2];                  // (NaN from the first sum on that is not finite: the row is lost)
+    float ref[2] = {0.f, 0.f};     // (NaN from the first sum on that is not finite: the row is lost)
     float scale[2] = {1.f, 1.f}, used[2] = {0.f, 0.f};     // 1 / unit; the sum since the last fold
     bool chosen = false, dirty = false, folded = false;
     float* slot = a.pw + (item + blockIdx.x) * (int64_t)(a.Sv * kCodebook * kTreeRG);

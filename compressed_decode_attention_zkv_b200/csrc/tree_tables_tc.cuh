@@ -4,7 +4,7 @@
 // CTA = 128 rows of one kv head (TMEM lanes) x some of its stages.  The rows are rotated once, scaled
 // and split into two fp16 planes (mma_split.cuh) in shared memory, in the tensor cores' K-major,
 // 128-byte-swizzled operand layout; the codewords come split from a kernel before, NB of a stage at a
-// time.  Per step one thread issues the three products lo hi, hi lo and hi hi (D / 16 tcgen05.mma of
+// time.  Per step one thread of a warp of its own issues the three products lo hi, hi lo and hi hi (D / 16 tcgen05.mma of
 // kind::f16 each, M = 128, N = NB) into one float32 accumulator of NB TMEM columns and commits them to an
 // mbarrier; the cross terms come first, so that their sum, 2^-11 of the rest, is complete before it
 // meets the large one.  While a step's products run, the step before is read from TMEM, scaled and
@@ -17,7 +17,9 @@
 
 namespace zkv {
 
-constexpr int kTtRows = 128, kTtThreads = 256;
+constexpr int kTtRows = 128;
+constexpr int kTtWork = 512;                 // threads that rotate, copy and read; one more warp issues
+constexpr int kTtThreads = kTtWork + 32;
 
 template <int D>
 struct TtCfg {
@@ -25,6 +27,7 @@ struct TtCfg {
   static constexpr int BUFS = D == 256 ? 1 : 2;                     // operand buffers
   static constexpr int P = D / 64;                                  // 128-byte panels of a row
   static constexpr int STEPS = kCodebook / NB;                      // per stage
+  static constexpr int GROUPS = NB >= 128 ? 4 : 2;                  // column groups of the reading warps
 };
 
 template <int D>
@@ -81,7 +84,7 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
     if (u < steps) {
       const int64_t first = ((int64_t)kvh * a.Sk + stage_of(u)) * kCodebook + u % C::STEPS * NB;
       auto& b = sm.b[u % C::BUFS];
-      for (int f = tid; f < NB * (D / 8); f += kTtThreads) {
+      for (int f = tid; f < NB * (D / 8); f += kTtWork) {
         const int n = f / (D / 8), gc = f % (D / 8), at = tt_swz(n, (gc & 7) * 8);
         cp_async16(&b[0][gc >> 3][at], a.books.hi + (first + n) * D + gc * 8);
         cp_async16(&b[1][gc >> 3][at], a.books.lo + (first + n) * D + gc * 8);
@@ -90,15 +93,15 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
     }
     cp_async_commit();
   };
-  // rows, rotated (float32 transform): warp w takes rows w, w + 8, ..., eight at a time
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
+  const bool works = tid < kTtWork;
+  // rows, rotated (float32 transform): warp w takes rows w, w + 16, ...
+  if (works) {
     float v[8][E], part[8], down_of;
     bool there[8];
     int i[8], g[8], b[8], present[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int r = warp + 8 * k + 64 * half, j = row0 + r;
+      const int r = warp + 16 * k, j = row0 + r;
       b[k] = a.by_rp.quotient(j);
       const int rho = j - b[k] * a.RP;
       i[k] = a.by_g.quotient(rho);
@@ -131,27 +134,27 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
     int own = 0;          // the norms of the eight rows at once
     const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
     down_of = exp2_int(-ex);
-    sm.qs[warp + 8 * own + 64 * half] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+    sm.qs[warp + 16 * own] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
-      const int r = warp + 8 * k + 64 * half;
+      const int r = warp + 16 * k;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int at = tt_swz(r, (e & 1) * 32 + lane);
         split(v[k][e] * down, sm.a[0][e >> 1][at], sm.a[1][e >> 1][at]);
       }
     }
-    if (half == 0) {
-      pdl_wait();         // (the kernel before splits the codewords)
-      copy(0);
-    }
   }
-  // reading a step: row = TMEM lane 32 (warp % 4) + lane, columns NB / 2 (warp / 4) ..
-  const int quarter = warp & 3, col0 = (warp >> 2) * (NB / 2), r = quarter * 32 + lane;
+  pdl_wait();             // (the kernel before splits the codewords)
+  if (works) copy(0);
+  // reading a step: row = TMEM lane 32 (warp % 4) + lane, columns of group warp / 4
+  constexpr int COLS = NB / C::GROUPS;
+  const int quarter = warp & 3, col0 = (warp >> 2) * COLS, r = quarter * 32 + lane;
+  const bool reads = works && warp < 4 * C::GROUPS;
   const int step = a.SKP * a.RG;
   float* out = nullptr;
-  if (r < rows) {
+  if (works && r < rows) {
     const int j = row0 + r, b = a.by_rp.quotient(j), rho = j - b * a.RP, rg = a.by_rg.quotient(rho);
     out = a.lut + (((int64_t)b * a.Hkv + kvh) * (a.RP / a.RG) + rg) * ((int64_t)kCodebook * step) + (rho - rg * a.RG);
   }
@@ -160,11 +163,11 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col0;
-  const float qs = sm.qs[r];
+  const float qs = sm.qs[r & (kTtRows - 1)];
   auto put = [&](int u) {
     float* o = out + (u % C::STEPS * NB + col0) * step + stage_of(u) * a.RG;
 #pragma unroll 1
-    for (int c = 0; c < NB / 2; c += 32) {
+    for (int c = 0; c < COLS; c += 32) {
       float v[32];
       tc_ld32(taddr + (uint32_t)((u & 1) * NB + c), v);
       if (out) {
@@ -191,7 +194,7 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
     }
     tc_fence_after();
     last = u;
-    if (tid == 0) {
+    if (tid == kTtWork) {
       const uint32_t b_base = (uint32_t)__cvta_generic_to_shared(&sm.b[u % C::BUFS][0][0][0]);
       const uint32_t acc = tmem + (uint32_t)((u & 1) * NB);
 #pragma unroll 1
@@ -215,22 +218,23 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
       asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar[u & 1])
                    : "memory");
     }
+    if (!works) continue;
     // the step that is read now: the one before, or with one operand buffer this one
     const int x = C::BUFS == 2 ? u - 1 : u;
     if (x >= 0) wait_for(x);
     copy(u + 1);                         // into the buffer that step u - 1 (or u) has left
-    if (x >= 0 && !late) put(x);
+    if (x >= 0 && !late && reads) put(x);
   }
-  if (C::BUFS == 2 && steps > 0 && !late) {
+  if (C::BUFS == 2 && steps > 0 && !late && works) {
     wait_for(steps - 1);
-    if (!late) put(steps - 1);
+    if (!late && reads) put(steps - 1);
   }
   cp_async_wait_all();
   if (late && lane == 0) set_error(err, ZKV_DEVERR_TIMEOUT);
   // the padded stages' entries are zero
   if (out && share == 0)
     for (int s = a.Sk; s < a.SKP; ++s)
-      for (int c = warp >> 2; c < kCodebook; c += 2) out[c * step + s * a.RG] = 0.f;
+      for (int c = warp >> 2; c < kCodebook; c += kTtWork / 128) out[c * step + s * a.RG] = 0.f;
   tc_fence_before();
   if (__syncthreads_or(late)) {
     // products still in flight get one more bounded wait before their columns are freed
