@@ -96,53 +96,51 @@ __device__ __forceinline__ void tree_tables_tc(const QueryTables& a, int64_t blk
   const bool works = tid < kTtWork;
   // rows, rotated (float32 transform): warp w takes rows w, w + 16, ...
   if (works) {
-    float v[8][E], part[8], down_of;
-    bool there[8];
-    int i[8], g[8], b[8], present[8];
+    // (short code that repeats: executed once, long straight code waits for its instructions)
+#pragma unroll 1
+    for (int k = 0; k < 8; k += 2) {
+      float v[2][E], part[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = warp + 16 * k, j = row0 + r;
-      b[k] = a.by_rp.quotient(j);
-      const int rho = j - b[k] * a.RP;
-      i[k] = a.by_g.quotient(rho);
-      g[k] = rho - i[k] * a.G;
-      there[k] = r < rows && rho < a.R;
-      if (!there[k]) b[k] = i[k] = g[k] = 0;
-      present[k] = a.n_query ? a.n_query[b[k]] : a.N;
-    }
+      for (int u = 0; u < 2; ++u) {
+        const int r = warp + 16 * (k + u), j = row0 + r;
+        int b = a.by_rp.quotient(j);
+        const int rho = j - b * a.RP;
+        int i = a.by_g.quotient(rho), g = rho - i * a.G;
+        const bool there = r < rows && rho < a.R;
+        if (!there) b = i = g = 0;
+        const int present = a.n_query ? a.n_query[b] : a.N;
+        const __half* qr = a.q + b * a.q_sb + i * a.q_sn + ((int64_t)kvh * a.G + g) * a.q_sh + lane;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const __half* qr = a.q + b[k] * a.q_sb + i[k] * a.q_sn + ((int64_t)kvh * a.G + g[k]) * a.q_sh + lane;
+        for (int e = 0; e < E; ++e) v[u][e] = __half2float(qr[e * 32]);
+        if (!there || i >= present)
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = __half2float(qr[e * 32]);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (!there[k] || i[k] >= present[k])
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = 0.f;
-      if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
-        const float* l = a.k_smooth + (int64_t)kvh * D + lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] *= l[e * 32];
+          for (int e = 0; e < E; ++e) v[u][e] = 0.f;
       }
-      fwht_warp_f32<D>(v[k], lane);
-      part[k] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) part[k] = fmaf(v[k][e], v[k][e], part[k]);
-    }
-    int own = 0;          // the norms of the eight rows at once
-    const int ex = split_exponent(sqrtf(TransposeSum<8, 8, 16>::run(part, lane, own)));
-    down_of = exp2_int(-ex);
-    sm.qs[warp + 16 * own] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+      for (int u = 0; u < 2; ++u) {
+        if (a.k_smooth) {   // the query absorbs the keys' smoothing: lambda * q
+          const float* l = a.k_smooth + (int64_t)kvh * D + lane;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<8>(k));
-      const int r = warp + 16 * k;
+          for (int e = 0; e < E; ++e) v[u][e] *= l[e * 32];
+        }
+        fwht_warp_f32<D>(v[u], lane);
+        part[u] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int at = tt_swz(r, (e & 1) * 32 + lane);
-        split(v[k][e] * down, sm.a[0][e >> 1][at], sm.a[1][e >> 1][at]);
+        for (int e = 0; e < E; ++e) part[u] = fmaf(v[u][e], v[u][e], part[u]);
+      }
+      int own = 0;          // the norms of both rows at once
+      const int ex = split_exponent(sqrtf(TransposeSum<2, 2, 16>::run(part, lane, own)));
+      const float down_of = exp2_int(-ex);
+      sm.qs[warp + 16 * (k + own)] = exp2_int(ex) * (float)(a.rot * (double)a.scale_log2);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<2>(u));
+        const int r = warp + 16 * (k + u);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int at = tt_swz(r, (e & 1) * 32 + lane);
+          split(v[u][e] * down, sm.a[0][e >> 1][at], sm.a[1][e >> 1][at]);
+        }
       }
     }
   }
