@@ -815,7 +815,10 @@ class _Prepared:
         self._device = torch.cuda.current_device()
 
     def __call__(self):
-        st = self._fn(*self._args, torch.cuda.current_stream(self._device).cuda_stream)
+        if torch.cuda.current_device() != self._device:     # (a kernel starts on the current device)
+            with torch.cuda.device(self._device):
+                return _Prepared.__call__(self)
+        st = self._fn(*self._args, torch.cuda.current_stream().cuda_stream)
         if st != ZKV_OK:
             raise ZkvError(self._name, st)
 

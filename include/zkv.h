@@ -521,8 +521,10 @@ int zkv_lse_merge_peers(const zkv_lse_merge_peers_params* p, void* stream);
  *   out      float32 [B][N][Hq][d] contiguous; lse float32 [B][N][Hq] contiguous
  *   the cache, its codebooks, k_smooth and the paged layout: as zkv_decode_params
  * 1 <= N <= 256; q, draft_k and draft_v rows 16-byte aligned (base and strides multiples of 8).
- * Scores are float32 sums of float32 table entries; weights are accumulated as integers whose
- * unit is 2^-29 of a scan tile's total or finer, and the output is normalised by their sum.
+ * Products have float32 accuracy (fp16 operands split in two).  Scores are float32 sums of float32
+ * table entries; weights are accumulated as integers whose unit is at most 2^-27 of the sum of a
+ * row's weights over the first tile of tokens that it was chosen for, and the output is normalised
+ * by their sum.  A row whose scores are not finite is NaN.
  * Workspace: zkv_tree_workspace_size(p) bytes, 256-byte aligned, no initial contents; it must
  *   not be shared by calls that run concurrently (two captured graphs replayed at once
  *   included).  It grows with B * Hkv * N * Hq / Hkv.

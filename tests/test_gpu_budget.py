@@ -329,6 +329,34 @@ def test_evict_bad_pages():
     assert (k[1] == 7).all() and np.array_equal(k[0], c["kc"][0, 0, :32]) and np.array_equal(k[2:].reshape(64, 2), c["kc"][0, 0, 64:])
 
 
+def test_evict_codes_in_place_and_totals_apart():
+    c = evict_case(57, B=2, Hkv=2, Sk=4, Sv=8, Tcap=5008, comp=[5000, 300])
+    k, v, n, acc = (_cuda(c[x]) for x in ("kc", "vc", "comp", "acc"))
+    acc_out, ln = torch.full_like(acc, 5), torch.zeros_like(n)
+    zkv.rvq_evict(k, v, n, acc, 700, 50, acc_out=acc_out, len_out=ln)
+    ko, vo, ao, lo, _ = evict_plain(c, 700, 50, (c["kc"], c["vc"], np.full_like(c["acc"], 5)))
+    same((k, v, acc_out, ln, acc, n), (ko, vo, ao, lo, c["acc"], c["comp"]))
+
+
+def test_budget_binding_refusals():
+    c = evict_case(58, B=1, Hkv=1, Sk=2, Sv=2, Tcap=64, comp=[64])
+    k, v, n, acc = (_cuda(c[x]) for x in ("kc", "vc", "comp", "acc"))
+    for kw in (dict(keep=0), dict(keep=65), dict(keep=4, recent=5)):
+        with pytest.raises(zkv.ZkvError):
+            zkv.rvq_evict(k, v, n, acc, **kw)
+    for kw in (dict(k_out=k), dict(acc_out=acc[:, :, :32]), dict(kept=torch.zeros(1, 1, 3, dtype=torch.int32, device="cuda")),
+               dict(k_out=k[:, :, :32].contiguous(), v_out=v[:, :, :32].contiguous()),
+               dict(block_table_out=torch.zeros(1, 1, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            zkv.rvq_evict(k, v, n, acc, 4, **kw)
+    w = weights_case(59, **WEIGHTS["one"])
+    args = [_cuda(w[x]) for x in ("q", "lse", "kc", "comp", "Ck")]
+    with pytest.raises(ValueError):
+        zkv.rvq_accumulate_weights(*args, torch.zeros(1, 1, 8, device="cuda"))
+    with pytest.raises(TypeError):
+        zkv.rvq_accumulate_weights(args[0], args[1].double(), *args[2:], _cuda(w["acc"]))
+
+
 def test_evict_is_replayed():
     c = evict_case(56, B=2, Hkv=2, Sk=4, Sv=4, Tcap=9000, comp=[9000, 5000])
     t = [_cuda(c[x]) for x in ("kc", "vc", "comp", "acc")]

@@ -150,6 +150,8 @@ CASES = {
     "many rows": dict(B=1, N=67, Hq=8, Hkv=1, d=64, Sk=4, Sv=4, Tcap=640, comp=[600], W=16, win=[16]),
     "many rows, d 128": dict(B=9, N=9, Hq=6, Hkv=2, d=128, Sk=3, Sv=2, Tcap=320, comp=[300, 0, 5, 320, 200, 128, 127, 1, 77], W=16, win=[16] * 9),
     "many rows, d 256": dict(B=1, N=50, Hq=4, Hkv=1, d=256, Sk=2, Sv=5, Tcap=320, comp=[311], W=16, win=[16]),
+    "256 drafts": dict(B=1, N=256, Hq=2, Hkv=1, d=64, Sk=2, Sv=2, Tcap=160, comp=[150], W=16, win=[16]),
+    "a wide window": dict(B=2, N=3, Hq=6, Hkv=2, d=128, Sk=2, Sv=2, Tcap=160, comp=[150, 0], W=1000, win=[1000, 777]),
     "longer": dict(B=2, N=2, Hq=4, Hkv=2, d=128, Sk=4, Sv=4, Tcap=20000, comp=[20000, 9001], W=16, win=[16, 16]),
 }
 
@@ -346,6 +348,62 @@ def test_tree_graphs_streams_and_repeats_agree():
     graphs[0].replay()
     torch.cuda.synchronize()
     check(new, step.out, step.lse)
+
+
+def test_tree_many_rows_repeat():
+    """128-row tables, several segments per row group: the same bits each time."""
+    c = make(24, B=2, N=26, Hq=32, Hkv=4, d=128, Sk=4, Sv=4, Tcap=9008, comp=[9001, 5000], W=16, win=[16, 3])
+    step = zkv.PreparedTreeAttn(*gpu_args(c), **gpu_kw(c))
+    o, l = (t.clone() for t in step())
+    for _ in range(5):
+        o2, l2 = step()
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+    few = {**c, "q": c["q"][:, :2], "dk": c["dk"][:, :2], "dv": c["dv"][:, :2], "N": 2, "nd": np.array([2, 2], np.int32)}
+    check(few, o[:, :2], l[:, :2])          # (a chain: the first drafts do not see the others)
+
+
+def test_tree_shares_a_workspace_in_stream_order():
+    a, b = make(25, **CASES["groups of 7"]), make(26, **CASES["many rows, d 128"])
+    need = max(zkv.tree_workspace_size(*gpu_args(c)) for c in (a, b))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")     # no initial contents are needed
+    sa = zkv.PreparedTreeAttn(*gpu_args(a), **gpu_kw(a), workspace=ws)
+    sb = zkv.PreparedTreeAttn(*gpu_args(b), **gpu_kw(b), workspace=ws)
+    wa, wb = plain(a), plain(b)
+    for _ in range(2):
+        sa()
+        sb()
+    check(a, sa.out, sa.lse, wa)
+    check(b, sb.out, sb.lse, wb)
+
+
+def test_binding_refusals():
+    c = make(27, **CASES["groups of 7"])
+    a, kw = gpu_args(c), gpu_kw(c)
+
+    def bad(i=None, t=None, error=ValueError, **k):
+        args = list(a)
+        if i is not None:
+            args[i] = t
+        with pytest.raises(error):
+            zkv.rvq_tree_attn(*args, **{**kw, **k})
+
+    bad(0, a[0][0])                                        # q without its batch axis
+    bad(0, a[0].float(), TypeError)
+    bad(0, a[0].transpose(2, 3))                           # rows not contiguous
+    bad(1, a[1][:, :3])                                    # fewer drafts than queries
+    bad(5, a[5][:1])                                       # one length
+    bad(5, a[5].long(), TypeError)
+    bad(6, a[6][:, :1])                                    # codebooks of other stages
+    bad(8, a[8][:1])
+    bad(mask=torch.ones(3, 3, dtype=torch.bool, device="cuda"))
+    bad(mask=torch.ones(5, 5, device="cuda"), error=TypeError)
+    bad(out=torch.zeros(1, device="cuda"))
+    bad(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"), error=zkv.ZkvError)
+    bad(max_comp_len=c["Tcap"] + 1, error=zkv.ZkvError)
+    bad(0, a[0].cpu())
+    with pytest.raises(zkv.ZkvError):                      # rows of 8 bytes apart
+        q = torch.zeros(2 * 5 * 14 * 132, dtype=torch.float16, device="cuda").as_strided((2, 5, 14, 128), (9240, 1848, 132, 1))
+        zkv.rvq_tree_attn(q, *a[1:], **kw)
 
 
 # ---------------------------------------------------------------------------------------------
