@@ -13,6 +13,7 @@
 // 64, the next chunk's loads in flight during a chunk's products.  With few blocks the chunks of a
 // stage are shared out over 2 or 4 blocks.  Every block splits the codewords that it uses; where many
 // would repeat that, the tree attention takes tree_tables_tc.cuh and codewords split before (SplitBooks).
+// 6 us for 8 rows or 32, d = 128, 4 stages: loads, rotation and one chunk's products, all latency.
 #pragma once
 
 #include "mma_split.cuh"

@@ -17,6 +17,17 @@
 //   3. tree_contract_kernel joins the slots of an item and contracts W_s with the value codebooks:
 //      one part per (stage, half of the codewords).
 //   4. tree_finish_kernel   sums the parts, rotates back, joins the dense part by log-sum-exp.
+//
+// Why tables and histograms here too: with R rows a (token, pair) costs R (Sk + Sv) / 32 shared-memory
+// passes of 128 bytes, gathers and counter additions together.  Reconstructing its key and value for
+// float32-accurate matrix products costs (Sk + Sv) d / 32 passes to gather float32 codewords and d / 16
+// to write the split vectors, whatever R is, and the codebooks of more than one stage do not fit in
+// shared memory.  So the histogram form is the cheaper one up to about R = d.
+//
+// Measured (B200): 8 sequences x 32640 tokens, 32 / 8 heads, d = 128, 4 + 4 stages, 16 drafts: 262 us a
+// call (split 6, tables 18, dense 15, scan 209, contraction 24, finish 8, partly side by side); one
+// sequence x 130816 tokens, 28 / 4 heads, 2 + 4 stages, 25 drafts: 149 us; 64 ragged sequences of 1024
+// .. 16384 tokens, 5 drafts: 361 us; one head, 960 tokens, 8 drafts: 25 us, five launches' latency.
 #include "query_tables.cuh"
 #include "tree_tables_tc.cuh"
 
@@ -133,7 +144,8 @@ __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
 
 // Dense attention of 16 rows of a pair over its window and its drafts: one pass over the keys in
 // steps of 64, 16 keys per warp with running maxima and sums of the warp's own; the four warps are
-// joined at the end.  Queries, keys and values are fp16 and their products exact; the weights are
+// joined at the end (64 rows per block and one warp per 16 rows: 38 us instead of 15 us at 64 pairs,
+// 64 rows, 144 keys: the chain of steps of one warp is what takes time).  Queries, keys and values are fp16 and their products exact; the weights are
 // split into two fp16 planes, and every 16 products are added up in float32.
 template <int D>
 __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeDenseSmem<D>& sm) {
@@ -408,6 +420,13 @@ __global__ void __launch_bounds__(kTtThreads, 1) tree_tables_tc_kernel(TreeArgs 
 // as exact integers in any order; when the sum of a row could pass 2^32 the counters are folded
 // into the slot (float32) and the unit chosen anew.  A rounding is half a unit, 2^-28 of a tile's
 // sum, per token.  A tile whose sum is above 2^64 is folded against its own maximum as the new ref.
+//
+// Bound: the shared-memory pipe.  At 8 x 32640 tokens, 64 rows: 209 us, 76 % of its passes used (40.5 M
+// of gathers, code reads and additions), 57 % of the issue slots, 2 CTAs of 12 warps per SM.  Steps
+// measured on that case: one row per lane 275 us; two rows per lane (half the address permutations and
+// code reads) with the codes copied ahead into shared memory instead of registers 185 us beside the
+// tables; 8 instead of 12 warps 6 % slower; 8 instead of 16 tokens per thread 30 % slower (the exchange
+// of sums per tile).
 template <int SKP, int SVP>
 struct TreeScan {
   static constexpr bool WIDE = SKP == 8 || SVP == 8;
@@ -839,6 +858,8 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
 // ---------------------------------------------------------------------------------------------
 // 3. Contraction with the value codebooks
 // ---------------------------------------------------------------------------------------------
+// 24 us at 512 rows per kv head, 8 heads, 4 stages, d = 128 (float32 FMA form: about 60 us): reading the
+// slots, 31 MB, and the join bound it; the tensor pipe is 23 % busy.
 // Block = 8 items of one kv head (64 rows) x 128 codewords of one stage: a product
 // [64 rows] x [128 codewords] x [D] with float32 accuracy (mma_split.cuh).  The codewords are read
 // and split before the wait for the scan.  Warp = item while the slots are joined by their

@@ -10,6 +10,9 @@
 // meets the large one.  While a step's products run, the step before is read from TMEM, scaled and
 // written, and the step after is copied (d = 256 has room for one operand buffer: there the copy
 // follows the products).
+// 18 us at 512 rows per kv head, 8 heads, 4 stages, d = 128; 35 us at 1536 rows (mma.sync with the
+// codewords split before: 25 and 67 us).  Writing the tables bounds it: 32 bytes per codeword, stage
+// and row group, about 3000 cycles a step beside 2800 of products.
 #pragma once
 
 #include "query_tables.cuh"
