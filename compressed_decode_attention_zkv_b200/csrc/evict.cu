@@ -153,12 +153,19 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   bool ties = false;           // more have it
   uint32_t keys[KPT];
   if (heavy > 0) {
-    // (no branch: all loads are in flight together; old > 0 here)
+    // (no branch per load: all are in flight together; old > 0 here)
     float x[KPT];
+    if (first + 32 * (KPT - 1) < old) {
+      const float* from = acc + first;
 #pragma unroll
-    for (int k = 0; k < KPT; ++k) x[k] = acc[min(first + 32 * k, old - 1)];
+      for (int k = 0; k < KPT; ++k) x[k] = __ldcg(from + 32 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) x[k] = __ldcg(acc + min(first + 32 * k, old - 1));
+    }
 #pragma unroll
     for (int k = 0; k < KPT; ++k) keys[k] = total_key(x[k]);
+    const bool full = __all_sync(0xffffffffu, first + 32 * (KPT - 1) < old);   // all of the warp's tokens are old
     uint32_t prefix = 0u, mask = 0u;
     uint32_t want = heavy;     // rank of the sought key among those that match the prefix
 #pragma unroll 1
@@ -169,10 +176,19 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
       uint32_t* hist = sm.hist[pass & 1];
       for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0u;
       __syncthreads();
+      if (pass == 0 && full) {
 #pragma unroll
-      for (int k = 0; k < KPT; ++k)
-        if (first + 32 * k < old && (keys[k] & mask) == prefix)
-          atomicAdd(&hist[(keys[k] >> shift) & (nb - 1)], 1u);
+        for (int k = 0; k < KPT; ++k) atomicAdd(&hist[keys[k] >> 21], 1u);
+      } else if (full) {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k)
+          if (((keys[k] ^ prefix) & mask) == 0u) atomicAdd(&hist[(keys[k] >> shift) & (nb - 1)], 1u);
+      } else {
+#pragma unroll
+        for (int k = 0; k < KPT; ++k)
+          if ((first + 32 * k < old) & (((keys[k] ^ prefix) & mask) == 0u))
+            atomicAdd(&hist[(keys[k] >> shift) & (nb - 1)], 1u);
+      }
       cluster_sync();
       // the cluster's counts from the highest digit down: thread i has digits 2 i and 2 i + 1
       static_assert(kEvBins == 2 * kEvThreads, "two digits per thread");
@@ -219,11 +235,19 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   } else {
     const int oldest = old - first, end = (int)n - first;      // of this lane's tokens: 32 k
     const uint32_t from = ties ? threshold + 1u : threshold;   // (an infinity's key is 2^32 - 2^23)
+    if (__all_sync(0xffffffffu, 32 * (KPT - 1) < oldest)) {
 #pragma unroll
-    for (int k = 0; k < KPT; ++k) {
-      const bool is_old = 32 * k < oldest;
-      const unsigned gt = __ballot_sync(0xffffffffu, ((!is_old) | (keys[k] >= from)) & (32 * k < end));
-      if (lane == k) gt_of = gt;
+      for (int k = 0; k < KPT; ++k) {
+        const unsigned gt = __ballot_sync(0xffffffffu, keys[k] >= from);
+        if (lane == k) gt_of = gt;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const bool is_old = 32 * k < oldest;
+        const unsigned gt = __ballot_sync(0xffffffffu, ((!is_old) | (keys[k] >= from)) & (32 * k < end));
+        if (lane == k) gt_of = gt;
+      }
     }
     if (ties)
 #pragma unroll
@@ -268,6 +292,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
 #pragma unroll 4
   for (int k = 0; k < KPT; ++k) {
     const uint32_t word = bits[warp * KPT + k];
+    if (!word) continue;
     if (word >> lane & 1u)
       src[pre[warp * KPT + k] + __popc(word & ((1u << lane) - 1u))] = (uint16_t)(warp * 32 * KPT + 32 * k + lane);
   }
@@ -283,15 +308,10 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
   // among the CTA's kept tokens, what get gave)
   auto each = [&](auto get, auto put) {
     for (uint32_t i0 = tid; i0 < kept_here; i0 += 4 * kEvThreads) {
-      uint32_t t[4];
       decltype(get(0u)) x[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t i = i0 + u * kEvThreads;
-        t[u] = begin + src[i < kept_here ? i : i0];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = get(t[u]);
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * kEvThreads < kept_here) x[u] = get(begin + src[i0 + u * kEvThreads]);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (i0 + u * kEvThreads < kept_here) put(i0 + u * kEvThreads, x[u]);
