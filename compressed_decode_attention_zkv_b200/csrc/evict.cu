@@ -16,10 +16,10 @@
 //   3. Copy.  Kept neighbours go to neighbouring places.  In place, a CTA first collects its kept
 //      rows in shared memory, four bytes of each at a time, and writes after a cluster barrier: by
 //      then every source of the (sequence, kv head) has been read.
-// 64 (sequence, kv head)s of 32640 tokens, an eighth kept: 23 us; 4 of 130816, a quarter kept: 27 us; one
-// of 960: 10 us.  Chains of latency bound it (cycles of one CTA of 16320 tokens: totals in 6300, three
-// passes 5000 each, of which counting 2200, cluster barrier 1000, remote counts 1300; flags and
-// offsets 5000, sources 2800, copies 4400), not bytes (14.6 MB: 10 % of the copy bandwidth).
+// 64 (sequence, kv head)s of 32640 tokens, an eighth kept: 18.5 us; 4 of 130816, a quarter kept: 23 us; one
+// of 960: 10 us.  Chains of latency bound it (cycles of one CTA of 16320 tokens: totals in 3600, three
+// passes 3500 to 4500 each, a cluster barrier and remote counts in each; flags and offsets 1700, sources
+// 3000, copies 3800), not bytes (14.6 MB: 12 % of the copy bandwidth).
 // The cluster has as many CTAs as the range needs and, up to 8, as leave no SM without work.
 #include <cooperative_groups.h>
 

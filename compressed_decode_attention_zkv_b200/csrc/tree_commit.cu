@@ -13,9 +13,9 @@
 // Kernel 1: the evictions of all sequences are numbered through (a prefix sum that every block
 // computes for itself), so a block encodes R evictions of one kv head and of K or V, from whichever
 // sequences.  R is 16 (one warp each); where that could make more blocks than SMs it is 32, since a
-// block's time is mostly that of the codewords it reads and splits.  Only the first eviction of a slot (k < W) reads the window, and its block then writes
-// the slot's last token; fill slots that no eviction takes are written apart.  So no slot is read by
-// one block and written by another.
+// block's time is mostly that of the codewords it reads and rounds.  Only the first eviction of a slot
+// (k < W) reads the window, and its block then writes the slot's last token; fill slots that no eviction
+// takes are written apart.  So no slot is read by one block and written by another.
 // Kernel 2 advances the lengths after all of kernel 1 has read them.
 //
 // Encode.  Per stage approximate distances ||c||^2 - 2 r . c of the R residuals to all 256 codewords
@@ -26,9 +26,11 @@
 // float32 row encoder for the rest, candidate_margin) of the smallest distance hold the nearest one.
 // One such codeword is the choice (for Gaussian codewords 15 times of 16); several are told apart by
 // float64 distances, ties to the lowest index, as zkv_rvq_encode decides.
-// 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages: 29 us; 64 sequences, up to 5: 45 us
-// (a cluster of 8 CTAs per 8 evictions, float32 distances: 50 and 176 us); one head, 2 + 2 stages: 15 us.
-// Bound by a block's chain: per chunk its loads, rounding and products, per stage the decision.
+// Chunks take turns in two buffers, so one is rounded while another's products run: one barrier a chunk.
+// 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages: 25 us; 64 sequences, up to 5: 40 us
+// (one buffer: 28 and 43; a cluster of 8 CTAs per 8 evictions, float32 distances: 50 and 176 us); one
+// head, 2 + 2 stages: 14.5 us.  The length update after it adds 3 us to each.
+// Bound by a block's chain: per chunk its rounding and products, per stage the decision.
 #include <cfloat>
 #include <cmath>
 
@@ -94,12 +96,12 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
 template <int D, int R>
 struct CommitSmem {
   static constexpr int CH = D == 256 ? 64 : 128;      // codewords per chunk (their loads fit in registers)
-  __half c[CH * D];                                   // codewords
+  __half c[2][CH * D];                                // codewords: chunks take turns
   __half x[R * D];                                    // residuals
   float r[R][D + 4];                        // residuals, float32
   float dist[R][kCodebook + 4];
-  float cn[kCodebook];                                // squared norms of the stage's codewords
-  float cs[CH];                                       // scales of the chunk's codewords
+  float cn[2][kCodebook];                             // squared norms of the codewords, by stage parity
+  float cs[2][CH];                                    // scales of the chunk's codewords
   float xs[R];                              // scales of the residuals
   float rn[R];                              // bound of their norms
   uint8_t code[R][kMaxStages];
@@ -148,6 +150,13 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
     }
   };
   if (blockIdx.x == 0) load(0);  // in flight while the evictions are numbered (later blocks may have none)
+  // a row's D halves per warp, E per lane
+  struct alignas(2 * E) Piece {
+    __half x[E];
+  };
+  auto move_row = [&](__half* dst, const __half* src) {
+    reinterpret_cast<Piece*>(dst)[lane] = reinterpret_cast<const Piece*>(src)[lane];
+  };
   if (tid < R) sm.row_b[tid] = -1;
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < p.B && base < row0 + R; b0 += kCommitThreads) {
@@ -225,70 +234,80 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
       put_row(r, y);
     }
     const int g = lane >> 2, t4 = lane & 3;
+    // chunk q from registers to shared memory: norms, scales, fp16
+    auto convert = [&](int q) {
+      // their norms: lane l gets codeword l % CW's (CW sums over the lanes at once)
+      float part[CW], down_of;
+#pragma unroll
+      for (int k = 0; k < CW; ++k) {
+        part[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[k] = fmaf(cw[k][e], cw[k][e], part[k]);
+      }
+      {
+        int own = 0;
+        const float ss = TransposeSum<CW, CW, 16>::run(part, lane, own);
+        // no element is larger than the norm: scale by its power of two
+        const int ex = split_exponent(sqrtf(ss));
+        down_of = exp2_int(-ex);
+        sm.cn[q / NC & 1][q % NC * CH + CW * warp + own] = ss;
+        sm.cs[q & 1][CW * warp + own] = exp2_int(ex);
+      }
+#pragma unroll
+      for (int k = 0; k < CW; ++k) {
+        const int c = CW * warp + k;
+        const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<CW>(k));
+        alignas(16) __half2 y[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) y[e / 2] = __floats2half2_rn(cw[k][e] * down, cw[k][e + 1] * down);
+        __half* at = sm.c[q & 1] + tile_at<D>(c, lane * E);
+        if constexpr (E == 2) *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(y);
+        else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(y);
+        else *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(y);
+      }
+    };
+    convert(0);
+    if (S * NC > 1) load(1);
     for (int s = 0; s < S; ++s) {
       for (int chunk = 0; chunk < NC; ++chunk) {
-        if (s + chunk > 0) __syncthreads();       // the previous chunk has been read
-        // their norms: lane l gets codeword l % CW's (CW sums over the lanes at once)
-        float part[CW], down_of;
-#pragma unroll
-        for (int k = 0; k < CW; ++k) {
-          part[k] = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) part[k] = fmaf(cw[k][e], cw[k][e], part[k]);
-        }
-        {
-          int own = 0;
-          const float ss = TransposeSum<CW, CW, 16>::run(part, lane, own);
-          // no element is larger than the norm: scale by its power of two
-          const int ex = split_exponent(sqrtf(ss));
-          down_of = exp2_int(-ex);
-          sm.cn[chunk * CH + CW * warp + own] = ss;
-          sm.cs[CW * warp + own] = exp2_int(ex);
-        }
-#pragma unroll
-        for (int k = 0; k < CW; ++k) {
-          const int c = CW * warp + k;
-          const float down = __shfl_sync(0xffffffffu, down_of, sum_owner<CW>(k));
-          alignas(16) __half2 y[E / 2];
-#pragma unroll
-          for (int e = 0; e < E; e += 2) y[e / 2] = __floats2half2_rn(cw[k][e] * down, cw[k][e + 1] * down);
-          __half* at = sm.c + tile_at<D>(c, lane * E);
-          if constexpr (E == 2) *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(y);
-          else if constexpr (E == 4) *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(y);
-          else *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(y);
-        }
+        const int q = s * NC + chunk;
+        // chunk q (and, at the first, the residuals) are there, and chunk q - 1 has been read
         __syncthreads();
-        if (s * NC + chunk + 1 < S * NC) load(s * NC + chunk + 1);
         if (8 * warp < CH) {         // 8 codewords per warp
           float acc[R / 16][2][4] = {};         // (two sums: neither waits for the other)
-#pragma unroll 2
+#pragma unroll 4
           for (int ks = 0; ks < D / 16; ks += 2) {
             uint32_t b[4];
-            frag_b2<D>(b, sm.c, 8 * warp, ks, lane);
+            frag_b2<D>(b, sm.c[q & 1], 8 * warp, ks, lane);
 #pragma unroll
-            for (int q = 0; q < R / 16; ++q)
+            for (int m = 0; m < R / 16; ++m)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 uint32_t x[4];
-                frag_a<D>(x, sm.x, 16 * q, ks + i, lane);
-                mma16816(acc[q][i], x, b[2 * i], b[2 * i + 1]);
+                frag_a<D>(x, sm.x, 16 * m, ks + i, lane);
+                mma16816(acc[m][i], x, b[2 * i], b[2 * i + 1]);
               }
           }
 #pragma unroll
-          for (int q = 0; q < R / 16; ++q)
+          for (int m = 0; m < R / 16; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int c = 8 * warp + 2 * t4 + (i & 1), r = 16 * q + g + 8 * (i >> 1);
-              const float dot = (acc[q][0][i] + acc[q][1][i]) * sm.cs[c] * sm.xs[r];
-              sm.dist[r][chunk * CH + c] = sm.cn[chunk * CH + c] - 2.f * dot;
+              const int c = 8 * warp + 2 * t4 + (i & 1), r = 16 * m + g + 8 * (i >> 1);
+              const float dot = (acc[m][0][i] + acc[m][1][i]) * sm.cs[q & 1][c] * sm.xs[r];
+              sm.dist[r][chunk * CH + c] = sm.cn[s & 1][chunk * CH + c] - 2.f * dot;
             }
+        }
+        // the next chunk meanwhile: a warp in its products leaves the issue slots to one that rounds
+        if (q + 1 < S * NC) {
+          convert(q + 1);
+          if (q + 2 < S * NC) load(q + 2);
         }
       }
       __syncthreads();
       // warp w decides rows w, w + 16: lane = codewords lane + 32 j
       float cmax = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cmax = fmaxf(cmax, sm.cn[32 * j + lane]);
+      for (int j = 0; j < 8; ++j) cmax = fmaxf(cmax, sm.cn[s & 1][32 * j + lane]);
       cmax = warp_max_f32(cmax);
 #pragma unroll 1
       for (int r = warp; r < R; r += 16) {
@@ -391,7 +410,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
       const int64_t last = k + (e - 1 - k) / p.Wcap * p.Wcap;     // the slot's last eviction
       const __half* src = token(b, p.Wcap - sm.row_s[r].wl + last);
       __half* dst = win + ((b * p.Hkv + h) * p.Wcap + (sm.row_s[r].head + k) % p.Wcap) * D;
-      for (int i = lane; i < D; i += 32) dst[i] = src[i];
+      move_row(dst, src);
     }
   }
   // fill tokens whose slot no eviction takes: the sequences are shared out over blocks and warps
@@ -405,7 +424,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
       if (s.evict > 0 && (slot - s.head + p.Wcap) % p.Wcap < s.evict) continue;
       const __half* src = token(b, i);
       __half* dst = win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
-      for (int x = lane; x < D; x += 32) dst[x] = src[x];
+      move_row(dst, src);
     }
   }
 }
