@@ -1263,7 +1263,8 @@ class RVQKVCache:
     decode step of attention, step() does both in one library call.  verify() attends with a tree
     of drafted tokens and commit() inserts the accepted ones; note_weights() adds up the attention
     that each compressed token receives (in ``acc``, made by its first call) and evict() keeps the
-    heaviest.  All state lives on the GPU; lengths never leave the device.
+    heaviest.  verify() and note_weights() share a workspace: calls and replayed graphs of them
+    must not run at once.  All state lives on the GPU; lengths never leave the device.
     k_smooth: optional float32 [Hkv, d] key smoothing factors (the key codebooks must have been
     trained on smoothed keys)."""
 
@@ -1288,6 +1289,7 @@ class RVQKVCache:
         self.max_comp_len = 0      # host-side bound used to size decode launches
         self.acc = None            # float32 [batch, Hkv, Tcap] attention-weight totals
         self._ws = None
+        self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
         """k, v: fp16 [B, Hkv, T, d] (same T for every sequence).  The last min(T, window)
@@ -1349,9 +1351,11 @@ class RVQKVCache:
                               k_smooth=self.k_smooth)
 
     def _scratch(self, need: int) -> torch.Tensor:
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
-        return self._ws
+        # outgrown ones are kept: a captured graph may hold their addresses (the sizes go by the
+        # cache's capacity, so only more queries than ever before outgrow one)
+        if not self._tree_ws or self._tree_ws[-1].numel() < need:
+            self._tree_ws.append(torch.empty(need, dtype=torch.uint8, device=self.k_codes.device))
+        return self._tree_ws[-1]
 
     def verify(self, q: torch.Tensor, draft_k: torch.Tensor, draft_v: torch.Tensor, mask=None,
                n_draft=None, softmax_scale=None, out=None, lse=None):
@@ -1360,7 +1364,7 @@ class RVQKVCache:
         [B, N, Hkv, d] -> (out float32 [B, N, Hq, d], lse float32 [B, N, Hq])."""
         args = (q, draft_k, draft_v, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv,
                 self.win_k, self.win_v, self.win_len)
-        need = tree_workspace_size(*args, max_comp_len=self.max_comp_len)
+        need = tree_workspace_size(*args)
         return rvq_tree_attn(*args, mask=mask, n_draft=n_draft, out=out, lse=lse,
                              max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
                              workspace=self._scratch(need), error_flag=self.error_flag,
@@ -1380,10 +1384,12 @@ class RVQKVCache:
         (rvq_accumulate_weights).  q and lse as attend() or verify() took and gave them, before
         any token was appended in between."""
         if self.acc is None:
+            if torch.cuda.is_current_stream_capturing():     # (replays would clear the totals)
+                raise RuntimeError("the first note_weights() makes the totals: call it before capture")
             self.acc = torch.zeros(self.k_codes.shape[:3], dtype=torch.float32,
                                    device=self.k_codes.device)
         args = (q, lse, self.k_codes, self.comp_len, self.Ck, self.acc)
-        need = weights_workspace_size(*args, max_comp_len=self.max_comp_len)
+        need = weights_workspace_size(*args)
         return rvq_accumulate_weights(*args, max_comp_len=self.max_comp_len,
                                       softmax_scale=softmax_scale, workspace=self._scratch(need),
                                       error_flag=self.error_flag, k_smooth=self.k_smooth)
@@ -1433,6 +1439,7 @@ class PQKVCache:
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_comp_len = 0
         self._ws = None
+        self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
         """k, v: fp16 [B, Hkv, T, d].  The last min(T, window) tokens go to the window, the

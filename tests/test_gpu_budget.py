@@ -442,3 +442,55 @@ def test_serving_loop(d, Hq, Hkv, S):
             assert cache.max_comp_len == keep
     out, lse = cache.attend(_cuda(new(Bn, Hq, d)))
     assert torch.isfinite(out).all() and torch.isfinite(lse).all() and cache.error_flag.item() == 0
+
+
+def _filled_cache(rng, W=16, T=700):
+    Bn, Hq, Hkv, d, S = 2, 8, 2, 128, 4
+    books = [_cuda((rng.standard_normal((Hkv, S, 256, d)) * 0.4).astype(np.float32)) for _ in range(2)]
+    cache = zkv.RVQKVCache(*books, batch=Bn, capacity=1024, window=W)
+    new = lambda *s: _cuda(rng.standard_normal(s).astype(np.float16))   # noqa: E731
+    cache.prefill(new(Bn, Hkv, T, d), new(Bn, Hkv, T, d))
+    drafts = lambda N: (new(Bn, N, Hq, d), new(Bn, N, Hkv, d), new(Bn, N, Hkv, d))   # noqa: E731
+    return cache, drafts
+
+
+def test_captured_verify_outlives_a_wider_one():
+    """A graph of verify() and attend() keeps its workspaces when later calls need larger ones."""
+    cache, drafts = _filled_cache(np.random.default_rng(62))
+    few, many = drafts(2), drafts(40)
+    q1 = few[0][:, 0].contiguous()
+    out, lse = cache.verify(*few)
+    first, _ = cache.attend(q1)
+    g = torch.cuda.CUDAGraph()
+    got, alone = torch.zeros_like(out), torch.zeros_like(first)
+    with torch.cuda.graph(g):
+        cache.verify(*few, out=got)
+        cache.attend(q1, out=alone)
+    sizes = [w.numel() for w in cache._tree_ws] + [cache._ws.numel()]
+    cache.verify(*many)
+    cache.note_weights(many[0], torch.zeros(many[0].shape[:3], device="cuda"))
+    # memory that the calls above may have given back, filled
+    fill = [torch.full((n,), 165, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and torch.equal(alone, first)
+    for f in fill:
+        assert (f == 165).all()
+
+
+def test_totals_are_not_made_in_a_capture():
+    cache, drafts = _filled_cache(np.random.default_rng(63))
+    q, dk, dv = drafts(2)
+    out, lse = cache.verify(q, dk, dv)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        with pytest.raises(RuntimeError):
+            cache.note_weights(q, lse)
+        cache.verify(q, dk, dv)
+    once = cache.note_weights(q, lse).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.note_weights(q, lse)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.acc, 2 * once)
