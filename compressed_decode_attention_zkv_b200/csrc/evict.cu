@@ -419,10 +419,10 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(EvictArgs a) {
 // after every CTA has read comp_len (len_out may be the same array)
 __global__ void evict_lengths_kernel(int B, int64_t Tcap, int64_t keep, const int32_t* comp_len,
                                      int32_t* len_out) {
-  pdl_wait();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  int64_t n = b < B ? comp_len[b] : 0;         // (the kernel before does not write it)
+  pdl_wait();
   if (b >= B) return;
-  int64_t n = comp_len[b];
   n = n < 0 ? 0 : n > Tcap ? Tcap : n;
   len_out[b] = (int32_t)(n < keep ? n : keep);
 }

@@ -14,7 +14,7 @@
 // computes for itself), so a block encodes R evictions of one kv head and of K or V, from whichever
 // sequences.  R is 16 (one warp each); where that could make more blocks than SMs it is 32, since a
 // block's time is mostly that of the codewords it reads and rounds.  Only the first eviction of a slot
-// (k < W) reads the window, and its block then writes the slot's last token; fill slots that no eviction
+// (k < W) reads the window, and its warp then writes the slot's last token; fill slots that no eviction
 // takes are written apart.  So no slot is read by one block and written by another.
 // Kernel 2 advances the lengths after all of kernel 1 has read them.
 //
@@ -27,9 +27,9 @@
 // One such codeword is the choice (for Gaussian codewords 15 times of 16); several are told apart by
 // float64 distances, ties to the lowest index, as zkv_rvq_encode decides.
 // Chunks take turns in two buffers, so one is rounded while another's products run: one barrier a chunk.
-// 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages: 25 us; 64 sequences, up to 5: 40 us
+// 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages: 24.7 us; 64 sequences, up to 5: 39 us
 // (one buffer: 28 and 43; a cluster of 8 CTAs per 8 evictions, float32 distances: 50 and 176 us); one
-// head, 2 + 2 stages: 14.5 us.  The length update after it adds 3 us to each.
+// head, 2 + 2 stages: 14 us.  The length update after it adds 1 us to each.
 // Bound by a block's chain: per chunk its rounding and products, per stage the decision.
 #include <cfloat>
 #include <cmath>
@@ -48,6 +48,10 @@ struct CommitState {
 // What sequence b commits; false (with the error bits in err) if it is left unchanged.
 __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, int64_t b,
                                              CommitState& s, int& err) {
+  const int32_t* path = p.path + b * p.M;
+  int32_t x[8];                      // (eight loads in flight, the first ones beside the state's)
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = path[min(q, p.M - 1)];
   s.n = p.n_accept[b];
   s.wl = p.win_len[b];
   s.head = p.win_head[b];
@@ -58,14 +62,13 @@ __device__ __forceinline__ bool commit_state(const zkv_tree_commit_params& p, in
     err = ZKV_DEVERR_DRAFT;
     return false;
   }
-  const int32_t* path = p.path + b * p.M;
   for (int i = 0; i < (int)s.n; i += 8) {
-    int32_t x[8];                    // (eight loads in flight, the last entry again behind it)
+    if (i > 0)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = path[min(i + q, (int)s.n - 1)];
+      for (int q = 0; q < 8; ++q) x[q] = path[min(i + q, p.M - 1)];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      if (x[q] < 0 || x[q] >= p.N) err = ZKV_DEVERR_DRAFT;
+      if (i + q < (int)s.n && (x[q] < 0 || x[q] >= p.N)) err = ZKV_DEVERR_DRAFT;
   }
   if (err) return false;
   if (s.wl < 0 || s.wl > p.Wcap) {
@@ -154,9 +157,9 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
   struct alignas(2 * E) Piece {
     __half x[E];
   };
-  auto move_row = [&](__half* dst, const __half* src) {
-    reinterpret_cast<Piece*>(dst)[lane] = reinterpret_cast<const Piece*>(src)[lane];
-  };
+  // whether this warp's first sequence (below) has free slots
+  const int64_t fill_b = (int64_t)blockIdx.x * 16 + warp;
+  const bool fills = fill_b < p.B && p.win_len[fill_b] != p.Wcap;
   if (tid < R) sm.row_b[tid] = -1;
   int64_t base = 0;
   for (int64_t b0 = 0; b0 < p.B && base < row0 + R; b0 += kCommitThreads) {
@@ -217,10 +220,20 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = 0.f;
       if (b >= 0) {
-        const int64_t k = sm.row_k[r], slot = (sm.row_s[r].head + k) % p.Wcap, wl = sm.row_s[r].wl;
+        // (fewer than 2^29 in all: 32-bit quotients)
+        const uint32_t W = (uint32_t)p.Wcap;
+        const int64_t k = sm.row_k[r], slot = ((uint32_t)sm.row_s[r].head + (uint32_t)k) % W, wl = sm.row_s[r].wl;
         const __half* x = k >= p.Wcap ? token(b, k - wl)               // the token of eviction k - W
                         : slot >= wl  ? token(b, slot - wl)            // a fill token
                                       : win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
+        // the slot's last token takes its place once the row has been read (by this warp alone)
+        Piece piece;
+        __half* dst = nullptr;
+        if (k < p.Wcap) {
+          const int64_t last = k + (uint32_t)(sm.row_s[r].evict - 1 - k) / W * W;     // the slot's last eviction
+          piece = reinterpret_cast<const Piece*>(token(b, p.Wcap - wl + last))[lane];
+          dst = win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
+        }
         double v[E];
         load_row_f64<E>(x, ZKV_DTYPE_F16, 0, lane, v);
         if (kind == 0 && p.k_smooth) {   // keys: x / lambda per channel before the rotation
@@ -230,6 +243,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
         fwht_warp_f64<D>(v, lane);
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (float)(v[e] * rot);
+        __syncwarp();
+        if (dst) reinterpret_cast<Piece*>(dst)[lane] = piece;
       }
       put_row(r, y);
     }
@@ -403,45 +418,36 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(zkv_tree_co
       }
       for (int s = 0; s < S; ++s) c[s] = sm.code[tid][s];
     }
-    // (the evicted slots have been read)
-    for (int r = warp; r < R; r += 16) {
-      if (sm.row_b[r] < 0 || sm.row_k[r] >= p.Wcap) continue;
-      const int64_t b = sm.row_b[r], k = sm.row_k[r], e = sm.row_s[r].evict;
-      const int64_t last = k + (e - 1 - k) / p.Wcap * p.Wcap;     // the slot's last eviction
-      const __half* src = token(b, p.Wcap - sm.row_s[r].wl + last);
-      __half* dst = win + ((b * p.Hkv + h) * p.Wcap + (sm.row_s[r].head + k) % p.Wcap) * D;
-      move_row(dst, src);
-    }
   }
   // fill tokens whose slot no eviction takes: the sequences are shared out over blocks and warps
-  for (int64_t b = (int64_t)blockIdx.x * 16 + warp; b < p.B; b += (int64_t)gridDim.x * 16) {
-    if (p.win_len[b] == p.Wcap) continue;      // no free slot
+  for (int64_t b = fill_b; b < p.B; b += (int64_t)gridDim.x * 16) {
+    if (b == fill_b ? !fills : p.win_len[b] == p.Wcap) continue;
     CommitState s;
     int err;
     if (!commit_state(p, b, s, err)) continue;
     for (int64_t i = 0; i < s.fill; ++i) {
       const int64_t slot = s.wl + i;
-      if (s.evict > 0 && (slot - s.head + p.Wcap) % p.Wcap < s.evict) continue;
+      if (s.evict > 0 && (uint32_t)(slot - s.head + p.Wcap) % (uint32_t)p.Wcap < s.evict) continue;
       const __half* src = token(b, i);
       __half* dst = win + ((b * p.Hkv + h) * p.Wcap + slot) * D;
-      move_row(dst, src);
+      reinterpret_cast<Piece*>(dst)[lane] = reinterpret_cast<const Piece*>(src)[lane];
     }
   }
 }
 
 __global__ void tree_commit_lengths_kernel(zkv_tree_commit_params p) {
-  pdl_wait();   // kernel 1 read the lengths before
   const int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= p.B) return;
   CommitState s;
-  int err;
-  const bool ok = commit_state(p, b, s, err);
+  int err = 0;
+  const bool ok = b < p.B && commit_state(p, b, s, err);     // (kernel 1 changes nothing of it)
   if (err) set_error(p.error_flag, err);
+  const int32_t head = ok ? (int32_t)((uint32_t)(s.head + s.evict) % (uint32_t)p.Wcap) : 0;
+  pdl_wait();   // every block of kernel 1 has read the lengths
   if (!ok) return;
   p.win_len[b] = (int32_t)(s.wl + s.fill);
   if (s.evict > 0) {
     p.comp_len[b] = (int32_t)(s.comp + s.evict);
-    p.win_head[b] = (int32_t)((s.head + s.evict) % p.Wcap);
+    p.win_head[b] = head;
   }
 }
 
@@ -475,6 +481,7 @@ extern "C" int zkv_rvq_tree_commit(const zkv_tree_commit_params* p, void* stream
   if (!supported_d(p->d)) return ZKV_ERR_UNSUPPORTED;
   if (p->Sk < 1 || p->Sk > kMaxStages || p->Sv < 1 || p->Sv > kMaxStages) return ZKV_ERR_UNSUPPORTED;
   if (p->Hkv > 65535 || p->B > 65535 || p->M > 256) return ZKV_ERR_UNSUPPORTED;
+  if (p->Wcap > (int64_t(1) << 28)) return ZKV_ERR_UNSUPPORTED;
   if (!p->draft_k || !p->draft_v || !p->path || !p->n_accept || !p->win_k || !p->win_v ||
       !p->win_len || !p->win_head || !p->comp_len || !p->k_codes || !p->v_codes ||
       !p->k_codebooks || !p->v_codebooks)

@@ -578,7 +578,7 @@ int zkv_rvq_tree_attn(const zkv_tree_params* p, void* workspace, size_t workspac
  * would go to a page outside the pool (ZKV_DEVERR_PAGE).
  * Layouts: draft_k / draft_v as zkv_tree_params; path int32 [B][M]; n_accept int32 [B]; the
  * state as zkv_append_params, updated in place.  Wcap >= 1, 1 <= N, 1 <= M <= 256.
- * No workspace.  Errors: INVALID_ARG, UNSUPPORTED (d, S, M), CUDA.
+ * No workspace.  Errors: INVALID_ARG, UNSUPPORTED (d, S, M, Wcap > 2^28), CUDA.
  */
 typedef struct {
   int B, N, M, Hkv, d, Sk, Sv;

@@ -103,7 +103,7 @@ def test_workspaces(L):
     (dict(M=0), INVALID), (dict(N=0), INVALID), (dict(Wcap=0), INVALID), (dict(d=32), UNSUPPORTED), (dict(Sk=9), UNSUPPORTED),
     (dict(M=257), UNSUPPORTED), (dict(path=None), INVALID), (dict(n_accept=None), INVALID), (dict(win_head=None), INVALID),
     (dict(k_sn=100), INVALID), (dict(draft_v=P + 8), INVALID), ({**PAGED, "page_tokens": 16}, INVALID),
-    (dict(B=0), INVALID), (dict(Tcap=-16), INVALID)])
+    (dict(B=0), INVALID), (dict(Tcap=-16), INVALID), (dict(Wcap=(1 << 28) + 1), UNSUPPORTED)])
 def test_commit(L, change, status):
     assert L.zkv_rvq_tree_commit(ctypes.byref(commit(**change)), None) == status
 
