@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kWtThreads, 2) weights_scan_kernel(WeightArgs 
     n = n < 0 ? 0 : a.Tcap;
   }
   if (n > a.max_comp) n = a.max_comp;
+  const int present = present_queries(a.qt.n_query, b, a.N);
+  if (a.qt.n_query && a.qt.n_query[b] != present && tid == 0) set_error(a.err, ZKV_DEVERR_DRAFT);
   const CodeRows kr = code_rows(a.k_codes, a.table, a.max_pages, a.n_pages, a.pshift, b, kvh, a.Hkv,
                                 a.Tcap, a.Sk, a.err);
   // this thread's tokens: t0 + u kWtThreads.  Their codes are in flight across the wait for the tables
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kWtThreads, 2) weights_scan_kernel(WeightArgs 
         if (tid < RG) {
           const int rho = rg * RG + tid;
           float x = -INFINITY;
-          if (rho < a.qt.R) {
+          if (rho < a.qt.R && rho / a.G < present) {
             const float l = a.lse[((int64_t)b * a.N + rho / a.G) * (a.Hkv * a.G) + (int64_t)kvh * a.G + rho % a.G];
             if (fabsf(l) < INFINITY) x = -l * kLog2e;
           }
@@ -294,7 +296,7 @@ extern "C" int zkv_rvq_accumulate_weights(const zkv_weights_params* p, void* wor
   a.NRG = q.RP / RG;
   q.q = reinterpret_cast<const __half*>(p->q);
   q.q_sb = p->q_sb; q.q_sn = p->q_sn; q.q_sh = p->q_sh;
-  q.Ck = p->k_codebooks; q.k_smooth = p->k_smooth;
+  q.n_query = p->n_draft; q.Ck = p->k_codebooks; q.k_smooth = p->k_smooth;
   q.scale_log2 = (float)((double)scale * 1.4426950408889634);
   q.rot = 1.0 / std::sqrt((double)p->d);
   q.set_divisors();

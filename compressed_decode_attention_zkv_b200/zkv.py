@@ -169,7 +169,7 @@ class WeightsParams(ctypes.Structure):
                 ("q", c_void_p), ("q_sb", c_int64), ("q_sn", c_int64), ("q_sh", c_int64),
                 ("lse", c_void_p), ("k_codes", c_void_p), ("comp_len", c_void_p),
                 ("k_codebooks", c_void_p), ("acc", c_void_p), ("error_flag", c_void_p),
-                ("k_smooth", c_void_p)] + _PAGED
+                ("k_smooth", c_void_p)] + _PAGED + [("n_draft", c_void_p)]
 
 
 class EvictParams(ctypes.Structure):
@@ -827,8 +827,8 @@ class PreparedTreeAttn(_Prepared):
     """rvq_tree_attn with its arguments validated and marshalled once (workspace included).  The
     tensors must keep their storage; max_comp_len must stay an upper bound of every comp_len for
     as long as the object is used.  Calling it runs one verification step on the current stream
-    and returns (out, lse); rows behind a sequence's drafts keep what they held (zeros in arrays
-    that the object makes)."""
+    and returns (out, lse); rows behind a sequence's drafts keep what they held (in arrays that the
+    object makes: zeros and an lse of -inf, which adds nothing to attention-weight totals)."""
 
     def __init__(self, q, draft_k, draft_v, k_codes, v_codes, comp_len, k_codebooks, v_codebooks,
                  win_k, win_v, win_len, mask=None, n_draft=None, out=None, lse=None,
@@ -841,7 +841,7 @@ class PreparedTreeAttn(_Prepared):
             out = torch.zeros(tuple(q.shape), dtype=torch.float32, device=q.device)
             p.out = _ptr(out)
         if lse is None:
-            lse = torch.zeros(tuple(q.shape[:3]), dtype=torch.float32, device=q.device)
+            lse = torch.full(tuple(q.shape[:3]), -math.inf, dtype=torch.float32, device=q.device)
             p.lse = _ptr(lse)
         need = _workspace_need("zkv_rvq_tree_attn", lib().zkv_tree_workspace_size, p)
         workspace = _workspace("zkv_rvq_tree_attn", need, workspace, q.device)
@@ -932,7 +932,7 @@ def rvq_tree_commit(draft_k, draft_v, path, n_accept, win_k, win_v, win_len, win
 # --------------------------------------------------------------------------------------------
 
 def _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len, softmax_scale,
-                    error_flag, k_smooth, block_table) -> WeightsParams:
+                    error_flag, k_smooth, block_table, n_draft) -> WeightsParams:
     if q.dim() == 3:
         q = q[:, None]
     if lse.dim() == 2:
@@ -944,18 +944,19 @@ def _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len, s
     qs = _rows(q, "q", (B, N, Hq, d))
     _need(lse, "lse", torch.float32)
     _shape(lse, "lse", (B, N, Hq))
-    _per_sequence(B, comp_len=comp_len)
+    _per_sequence(B, comp_len=comp_len, n_draft=n_draft)
     _books(k_codebooks, "k_codebooks", Hkv, Sk, d)
     _need(acc, "acc", torch.float32)
     _shape(acc, "acc", (B, Hkv, Tcap))
     _one_device(q=q, lse=lse, k_codes=k_codes, comp_len=comp_len, k_codebooks=k_codebooks,
-                acc=acc, error_flag=error_flag, k_smooth=k_smooth, block_table=block_table)
+                acc=acc, error_flag=error_flag, k_smooth=k_smooth, block_table=block_table,
+                n_draft=n_draft)
     return WeightsParams(B=B, N=N, Hq=Hq, Hkv=Hkv, d=d, Sk=Sk, Tcap=Tcap,
                          max_comp_len=Tcap if max_comp_len is None else int(max_comp_len),
                          softmax_scale=0.0 if softmax_scale is None else float(softmax_scale),
                          q=_ptr(q), q_sb=qs[0], q_sn=qs[1], q_sh=qs[2], lse=_ptr(lse),
                          k_codes=_ptr(k_codes), comp_len=_ptr(comp_len),
-                         k_codebooks=_ptr(k_codebooks), acc=_ptr(acc),
+                         k_codebooks=_ptr(k_codebooks), acc=_ptr(acc), n_draft=_ptr(n_draft),
                          error_flag=_flag(error_flag),
                          k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged)
 
@@ -964,7 +965,7 @@ def weights_workspace_size(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp
                            block_table=None) -> int:
     """Bytes of device workspace that rvq_accumulate_weights needs for these shapes."""
     p = _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len, None, None,
-                        None, block_table)
+                        None, block_table, None)
     return _workspace_need("zkv_weights_workspace_size", lib().zkv_weights_workspace_size, p)
 
 
@@ -975,14 +976,14 @@ class PreparedAccumulate(_Prepared):
 
     def __init__(self, q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len=None,
                  softmax_scale=None, workspace: torch.Tensor | None = None, error_flag=None,
-                 k_smooth=None, block_table=None):
+                 k_smooth=None, block_table=None, n_draft=None):
         p = _weights_params(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len,
-                            softmax_scale, error_flag, k_smooth, block_table)
+                            softmax_scale, error_flag, k_smooth, block_table, n_draft)
         need = _workspace_need("zkv_rvq_accumulate_weights", lib().zkv_weights_workspace_size, p)
         workspace = _workspace("zkv_rvq_accumulate_weights", need, workspace, q.device)
         self.acc = acc
         self._set("zkv_rvq_accumulate_weights", p, workspace, q, lse, k_codes, comp_len,
-                  k_codebooks, acc, error_flag, k_smooth, block_table)
+                  k_codebooks, acc, error_flag, k_smooth, block_table, n_draft)
 
     def __call__(self):
         super().__call__()
@@ -991,13 +992,16 @@ class PreparedAccumulate(_Prepared):
 
 def rvq_accumulate_weights(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len=None,
                            softmax_scale=None, workspace=None, error_flag=None, k_smooth=None,
-                           block_table=None):
+                           block_table=None, n_draft=None):
     """acc[b, kvh, t] += the attention weight that compressed token t received from the queries
     (see include/zkv.h).  q fp16 [B, N, Hq, d] (or [B, Hq, d]: one query each) and lse float32
     [B, N, Hq] (or [B, Hq]) as rvq_tree_attn / rvq_decode_attn took and gave them; acc float32
-    [B, Hkv, Tcap].  A query whose lse is infinite or NaN adds nothing.  Returns acc."""
+    [B, Hkv, Tcap].  A query whose lse is infinite or NaN adds nothing, nor does one behind the
+    sequence's drafts (n_draft int32 [B], as rvq_tree_attn took it; None: N everywhere).
+    Returns acc."""
     return PreparedAccumulate(q, lse, k_codes, comp_len, k_codebooks, acc, max_comp_len,
-                              softmax_scale, workspace, error_flag, k_smooth, block_table)()
+                              softmax_scale, workspace, error_flag, k_smooth, block_table,
+                              n_draft)()
 
 
 class PreparedEvict(_Prepared):
@@ -1361,7 +1365,8 @@ class RVQKVCache:
                n_draft=None, softmax_scale=None, out=None, lse=None):
         """Attention of N drafted tokens per sequence over the cache and over each other, which
         leaves the cache as it is (rvq_tree_attn).  q fp16 [B, N, Hq, d], draft_k / draft_v fp16
-        [B, N, Hkv, d] -> (out float32 [B, N, Hq, d], lse float32 [B, N, Hq])."""
+        [B, N, Hkv, d] -> (out float32 [B, N, Hq, d], lse float32 [B, N, Hq]).  Rows behind a
+        sequence's n_draft drafts keep what a given out or lse held; otherwise 0 and -inf."""
         args = (q, draft_k, draft_v, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv,
                 self.win_k, self.win_v, self.win_len)
         need = tree_workspace_size(*args)
@@ -1379,10 +1384,12 @@ class RVQKVCache:
                         self.error_flag, self.k_smooth)
         self.max_comp_len = min(self.max_comp_len + path.shape[1], self.Tcap)
 
-    def note_weights(self, q: torch.Tensor, lse: torch.Tensor, softmax_scale=None):
+    def note_weights(self, q: torch.Tensor, lse: torch.Tensor, softmax_scale=None, n_draft=None):
         """Adds the attention weight of q over the compressed tokens to ``acc``
         (rvq_accumulate_weights).  q and lse as attend() or verify() took and gave them, before
-        any token was appended in between."""
+        any token was appended in between.  Rows that shall not count (rejected drafts) need an lse
+        of +inf; rows behind the drafts do not count where verify() made the array of lse, and in
+        another array if n_draft is given as verify() took it."""
         if self.acc is None:
             if torch.cuda.is_current_stream_capturing():     # (replays would clear the totals)
                 raise RuntimeError("the first note_weights() makes the totals: call it before capture")
@@ -1392,7 +1399,8 @@ class RVQKVCache:
         need = weights_workspace_size(*args)
         return rvq_accumulate_weights(*args, max_comp_len=self.max_comp_len,
                                       softmax_scale=softmax_scale, workspace=self._scratch(need),
-                                      error_flag=self.error_flag, k_smooth=self.k_smooth)
+                                      error_flag=self.error_flag, k_smooth=self.k_smooth,
+                                      n_draft=n_draft)
 
     def evict(self, keep: int, recent: int = 0, kept=None):
         """Keeps at most ``keep`` compressed tokens per sequence and kv head: the ``recent`` newest

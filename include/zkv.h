@@ -74,8 +74,9 @@ const char* zkv_status_string(int status);
 
 /* Library ABI version (major * 100 + minor): 1.01 adds the serving step, the paged layout,
  * key smoothing, product VQ and the context-parallel combines to 1.00's encode / decode; 1.02
- * the tree attention, the path commit, the attention-weight totals and the eviction. */
-#define ZKV_VERSION 102
+ * the tree attention, the path commit, the attention-weight totals and the eviction; 1.03
+ * n_draft of the attention-weight totals. */
+#define ZKV_VERSION 103
 int zkv_version(void);
 
 /*
@@ -511,7 +512,7 @@ int zkv_lse_merge_peers(const zkv_lse_merge_peers_params* p, void* stream);
  *   out[b][i][h] = softmax(softmax_scale * q[b][i][h] . keys) . values         (float32)
  *   lse[b][i][h] = natural log of sum exp(softmax_scale * q . k)              (float32, or NULL)
  * A row without any key gives out = 0 and lse = -inf.  Rows i >= n_draft[b] of out and lse are
- * not written.  Results do not depend on the order in which thread blocks run.
+ * not written: set them to 0 and -inf beforehand where something reads them.  Results do not depend on the order in which thread blocks run.
  * Layouts (strides in elements; the last index, d or j, is contiguous):
  *   q        fp16, (b, i, h) at q + b*q_sb + i*q_sn + h*q_sh
  *   draft_k, draft_v fp16, (b, i, kvh) at x + b*k_sb + i*k_sn + kvh*k_sh (v_sb, ... for values)
@@ -616,7 +617,9 @@ int zkv_rvq_tree_commit(const zkv_tree_commit_params* p, void* stream);
  * lse is what the attention over the whole context gave (zkv_rvq_decode_attn,
  * zkv_rvq_tree_attn), so each query hands out a total weight of one over the context.  A query
  * whose lse is -inf (it attended to nothing), +inf or NaN adds nothing: set +inf for the rows
- * that shall not count, such as rejected drafts.  Entries at t >= comp_len[b] are not touched.
+ * that shall not count, such as rejected drafts.  With n_draft (int32 [B] on the device, or NULL:
+ * N everywhere) only the queries i < n_draft[b] count, as zkv_rvq_tree_attn computes only theirs:
+ * rows of q and lse behind them may hold anything.  Entries at t >= comp_len[b] are not touched.
  * Layouts: q as zkv_tree_params; lse float32 [B][N][Hq] contiguous; acc float32
  * [B][Hkv][Tcap] contiguous (by position in both code layouts); the rest as zkv_decode_params.
  * Workspace: zkv_weights_workspace_size(p) bytes, 256-byte aligned, as zkv_rvq_tree_attn's.
@@ -637,6 +640,7 @@ typedef struct {
   const float* k_smooth;
   const int32_t* block_table;
   int64_t page_tokens, max_pages, n_pages;
+  const int32_t* n_draft;
 } zkv_weights_params;
 
 size_t zkv_weights_workspace_size(const zkv_weights_params* p);
