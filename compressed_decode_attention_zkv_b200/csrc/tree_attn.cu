@@ -416,10 +416,16 @@ __global__ void __launch_bounds__(kTtThreads, 1) tree_tables_tc_kernel(TreeArgs 
 //
 // Weights.  p = 2^(score - ref) with ref the row's maximum over the first tokens of the segment.  The block sums p
 // per row over the tile before it adds any (one barrier), so a row's unit can be chosen: a power
-// of two with the first tile's sum at 2^27 .. 2^28 units.  Counters then take u = p / unit, rounded,
+// of two with the first tile's sum at 2^27 .. 2^28 units.  Counters then take u = floor(p / unit + d)
 // as exact integers in any order; when the sum of a row could pass 2^32 the counters are folded
-// into the slot (float32) and the unit chosen anew.  A rounding is half a unit, 2^-28 of a tile's
-// sum, per token.  A tile whose sum is above 2^64 is folded against its own maximum as the new ref.
+// into the slot (float32) and the unit chosen anew.  d in [0, 1) is an offset of the token's place:
+// the 8 slots x NW warps of a tile have equally spaced ones, which turn from tile to tile, so that
+// equal weights below a unit are counted as often as their sum asks for.  (Rounding to the nearest
+// loses them all: for a first token and 32639 of 2^-28.1 of its weight each that is 1.1e-4 of the
+// sum and 1.6e-4 of the output, with the offsets 2e-7 and nothing in the float32 lse; the times are
+// the same.)  A weight is off by less than a unit, 2^-27 of a tile's sum, its mean over the places by
+// nothing; no weight (p = 0) counts nothing.  A tile whose sum is above 2^64 is
+// folded against its own maximum as the new ref.
 //
 // Bound: the shared-memory pipe.  At 8 x 32640 tokens, 64 rows: 209 us, 76 % of its passes used (40.5 M
 // of gathers, code reads and additions), 57 % of the issue slots, 2 CTAs of 12 warps per SM.  Steps
@@ -441,6 +447,17 @@ struct TreeScan {
   static constexpr int CODES = 32 * (kTreeTK / 4) * (SKP + SVP);   // bytes of a warp's part of a tile
   static constexpr int SMEM = TABLES + SUMS + 2 * NW * CODES;
   static constexpr int KW = SKP <= 4 ? 1 : 2, VW = SVP <= 4 ? 1 : 2;   // code words per token
+
+  // Offsets of the roundings in units of 2^-32: place (slot h, warp w) is one of 8 NW equal steps,
+  // with the slots of a warp and the warps of a slot spread over all of them, too.
+  static constexpr uint32_t STEP = 0x80000000u / (4 * NW);
+  __device__ __forceinline__ static uint32_t place(uint32_t h, uint32_t w) {
+    const uint32_t at = NW == 12 ? 4u * ((3u * h + 2u * w) % 24u) + (h >> 1) : 8u * ((2u * h + w) % 16u) + h;
+    return at * STEP + STEP / 2;
+  }
+  // The turn from tile to tile, near the golden ratio's 0.618 and such that the steps themselves
+  // move by 0.618 of one (59.618 / 96, 79.618 / 128)
+  static constexpr uint32_t TURN = NW == 12 ? 2667265689u : 2671537907u;
 };
 
 // The codes of four tokens from the warp's copy (p: the first one's S bytes; 4-byte aligned).  EXACT:
@@ -527,6 +544,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
   for (int i = 0; i < (SKP + 1) / 2; ++i) asm volatile("" : "+r"(kcol[i]));
 #pragma unroll
   for (int i = 0; i < (SVP + 1) / 2; ++i) asm volatile("" : "+r"(vcol[0][i]), "+r"(vcol[1][i]));
+  const uint32_t place = C::place((uint32_t)h, (uint32_t)warp);
   pdl_wait();
   const int64_t per = a.pre[a.B + 1];
   const int64_t items_per_b = (int64_t)a.Hkv * a.NRG;
@@ -752,6 +770,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       return sum;
     };
     auto tile_add = [&](auto ex, uint32_t tile, int q, const float2 (&p)[kTreeTK], const float (&mul)[2]) {
+      const float off = (float)((place + (tile - t0) / C::TILE * C::TURN) >> 8) * 0x1p-24f;     // below 1
 #pragma unroll
       for (int k = 0; k < kTreeTK / 4; ++k) {
         if (tile + (k * C::NW + warp) * 32 >= tend) break;
@@ -759,8 +778,8 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
         value_codes(ex, q, k, w);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint32_t u0 = __float2uint_rn(p[4 * k + u].x * mul[0]);
-          const uint32_t u1 = __float2uint_rn(p[4 * k + u].y * mul[1]);
+          const uint32_t u0 = __float2uint_rd(fmaf(p[4 * k + u].x, mul[0], off));
+          const uint32_t u1 = __float2uint_rd(fmaf(p[4 * k + u].y, mul[1], off));
           const uint32_t ua = swap ? u1 : u0, ub = swap ? u0 : u1;
           uint32_t x[C::VW];
 #pragma unroll
@@ -813,7 +832,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
       for (int j = 0; j < 2; ++j) {
         bad[j] = !(sum[j] < 3e38f);
         if (bad[j]) ref[j] = NAN;
-        full = full || (!bad[j] && used[j] + sum[j] * scale[j] + (float)(C::TILE / 2) > 4.0e9f);
+        full = full || (!bad[j] && used[j] + sum[j] * scale[j] + (float)C::TILE > 4.0e9f);
       }
       if (__any_sync(0xffffffffu, full || !chosen)) {
         if (dirty) {
@@ -837,7 +856,7 @@ __global__ void __launch_bounds__(TreeScan<SKP, SVP>::THREADS, TreeScan<SKP, SVP
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         mul[j] = bad[j] ? 0.f : scale[j];        // (inf and NaN times 0 convert to 0)
-        used[j] += sum[j] * mul[j] + (float)(C::TILE / 2);
+        used[j] += sum[j] * mul[j] + (float)C::TILE;
       }
       dirty = true;
       if (exact) tile_add(std::true_type{}, tile, q, p, mul);

@@ -524,8 +524,10 @@ int zkv_lse_merge_peers(const zkv_lse_merge_peers_params* p, void* stream);
  * 1 <= N <= 256; q, draft_k and draft_v rows 16-byte aligned (base and strides multiples of 8).
  * Products have float32 accuracy (fp16 operands split in two).  Scores are float32 sums of float32
  * table entries; weights are accumulated as integers whose unit is at most 2^-27 of the sum of a
- * row's weights over the first tile of tokens that it was chosen for, and the output is normalised
- * by their sum.  A row whose scores are not finite is NaN.
+ * row's weights over the first tile of tokens that it was chosen for (1536 or 2048 tokens), and the
+ * output is normalised by their sum.  A weight is rounded up or down by the place of its token, each
+ * in proportion, so that many light tokens beside a heavy one keep their weight; n of them are off
+ * by some 2^-28 sqrt(n) of the row's sum together, n 2^-27 if every one fell to the same side.  A row whose scores are not finite is NaN.
  * Workspace: zkv_tree_workspace_size(p) bytes, 256-byte aligned, no initial contents; it must
  *   not be shared by calls that run concurrently (two captured graphs replayed at once
  *   included).  It grows with B * Hkv * N * Hq / Hkv.
