@@ -89,6 +89,7 @@ __device__ __forceinline__ int64_t comp_tokens(const int32_t* comp_len, int b, i
 constexpr int kTreeDenseThreads = 128;
 constexpr int kTreeDenseRows = 16;    // query rows of a dense block
 constexpr int kTreeDenseKeys = 64;    // keys per step, 16 per warp
+constexpr float kTreeDenseUp = 32768.f;   // of the weights in the products: 2^15 is the largest, 2^-40 the last
 
 template <int D>
 struct TreeDenseSmem {
@@ -145,8 +146,10 @@ __device__ __forceinline__ void tree_partition(const TreeArgs& a) {
 // Dense attention of 16 rows of a pair over its window and its drafts: one pass over the keys in
 // steps of 64, 16 keys per warp with running maxima and sums of the warp's own; the four warps are
 // joined at the end (64 rows per block and one warp per 16 rows: 38 us instead of 15 us at 64 pairs,
-// 64 rows, 144 keys: the chain of steps of one warp is what takes time).  Queries, keys and values are fp16 and their products exact; the weights are
-// split into two fp16 planes, and every 16 products are added up in float32.
+// 64 rows, 144 keys: the chain of steps of one warp is what takes time).  Queries, keys and values are fp16 and their products exact; the weights, times
+// 2^15, are split into two fp16 planes, and every 16 products are added up in float32.  (fp16 ends at
+// 2^-25: without the factor every key lighter than that of its warp's heaviest was lost, with 4095 keys
+// of 2^-25.5 and eight times its value 1.6e-4 of the output.)
 template <int D>
 __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeDenseSmem<D>& sm) {
   constexpr int NT = D / 8;                    // output tiles of 8 columns
@@ -287,9 +290,10 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
       const float x = ex2_approx(s[i >> 1][2 * (i & 1)] - ref[i & 1]);
       const float y = ex2_approx(s[i >> 1][2 * (i & 1) + 1] - ref[i & 1]);
       l[i & 1] += x + y;
-      const __half2 hi = __floats2half2_rn(x, y);
+      const float xs = x * kTreeDenseUp, ys = y * kTreeDenseUp;
+      const __half2 hi = __floats2half2_rn(xs, ys);
       const float2 back = __half22float2(hi);
-      const __half2 lo = __floats2half2_rn(x - back.x, y - back.y);
+      const __half2 lo = __floats2half2_rn(xs - back.x, ys - back.y);
       ph[i] = *reinterpret_cast<const uint32_t*>(&hi);
       pl[i] = *reinterpret_cast<const uint32_t*>(&lo);
     }
@@ -344,6 +348,8 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) y[e] = fmaf(os[(k * kTreeDenseRows + r) * D + e * 32 + lane], f, y[e]);
     }
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) y[e] *= 1.f / kTreeDenseUp;
     if (sm.odd)
       for (int key = 0; key < nd; ++key) {
         if (a.mask ? a.mask[b * a.m_sb + i * a.m_sn + key] == 0 : key > i) continue;
