@@ -350,6 +350,18 @@ __device__ __forceinline__ void tree_dense(const TreeArgs& a, int64_t blk, TreeD
     }
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) y[e] *= 1.f / kTreeDenseUp;
+    // An infinity of the window has become NaN in a plane of the weights that is zero: a dimension that
+    // holds such values is their sum, whatever the weights are.
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      if (!(fabsf(y[e]) < INFINITY)) {
+        float all = 0.f;
+        for (int64_t t = 0; t < wl; ++t) {
+          const float v = __half2float(a.win_v[(pair * a.Wcap + t) * D + e * 32 + lane]);
+          if (!(fabsf(v) < INFINITY)) all += v;
+        }
+        if (all != 0.f) y[e] = all;
+      }
     if (sm.odd)
       for (int key = 0; key < nd; ++key) {
         if (a.mask ? a.mask[b * a.m_sb + i * a.m_sn + key] == 0 : key > i) continue;

@@ -1,4 +1,4 @@
-"""Tree attention over an fp16 window: many light keys beside a heavy one."""
+"""Tree attention over an fp16 window: many light keys beside a heavy one, values that are not finite."""
 import math
 
 import numpy as np
@@ -42,3 +42,29 @@ def test_light_window_keys_add_up():
     # the one lane's sum that holds the large weight, splits of 2^-22
     assert (out.double() - want).abs().max().item() <= 130 * 2.0 ** -24 + tail / 16 + 2.0 ** -21
     assert (lse.double() - top - math.log1p(tail)).abs().max().item() <= 64 * 2.0 ** -24 + tail / 16 + SCORES
+
+
+def test_infinities_in_the_window():
+    """What a visible window value holds reaches the output as the sum has it: an infinity of little weight too,
+    NaN for two of opposite sign, and nothing of it in the other dimensions."""
+    rng = np.random.default_rng(8)
+    W, N, Hkv, G, T = 150, 5, 2, 4, 300
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float16)).cuda()   # noqa: E731
+    q, dk, dv = new(1, N, Hkv * G, D), new(1, N, Hkv, D), new(1, N, Hkv, D)
+    wk, wv = new(1, Hkv, W, D), new(1, Hkv, W, D)
+    q[..., 0] = 8
+    wk[:, :, 3, 0] = -30                     # about 2^-43 of the others
+    kc = torch.from_numpy(rng.integers(0, 256, (1, Hkv, 304, 2)).astype(np.uint8)).cuda()
+    books = torch.from_numpy((rng.standard_normal((Hkv, 2, 256, D)) * 0.3).astype(np.float32)).cuda()
+    one = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")   # noqa: E731
+    plain, _ = zkv.rvq_tree_attn(q, dk, dv, kc, kc, one(T), books, books, wk, wv, one(W - 1))
+    bad = wv.clone()
+    bad[:, :, 3, 5], bad[:, :, 70, 9] = math.inf, -math.inf
+    bad[:, :, 1, 11], bad[:, :, 140, 11] = math.inf, -math.inf
+    bad[:, :, 64, 20] = math.nan
+    bad[:, :, W - 1] = math.nan              # behind the window
+    out, lse = zkv.rvq_tree_attn(q, dk, dv, kc, kc, one(T), books, books, wk, bad, one(W - 1))
+    assert (out[..., 5] == math.inf).all() and (out[..., 9] == -math.inf).all()
+    assert torch.isnan(out[..., 11]).all() and torch.isnan(out[..., 20]).all()
+    rest = [i for i in range(D) if i not in (5, 9, 11, 20)]
+    assert torch.equal(out[..., rest], plain[..., rest]) and torch.isfinite(lse).all()
