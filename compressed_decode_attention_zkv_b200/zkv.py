@@ -1260,7 +1260,30 @@ def lse_merge_peers(part_out_ptrs: torch.Tensor, part_lse_ptrs: torch.Tensor,
     return out, lse
 
 
-class RVQKVCache:
+class _HostBound:
+    """max_comp_len of a cache: the host's bound of lengths that live on the device.  It follows the
+    calls; what a capture records runs at its replays, which are not seen here."""
+
+    max_comp_len = 0
+    _replayed = False          # a capture holds a call that changes the lengths
+
+    def _grown(self, bound: int):
+        """Every length is at most ``bound`` from now on, or any length after a replay."""
+        self._replayed = self._replayed or torch.cuda.is_current_stream_capturing()
+        self.max_comp_len = self.Tcap if self._replayed else min(bound, self.Tcap)
+
+    def _shrunk(self, bound: int):
+        """The same of a call that lets no length grow; a captured one has not run yet."""
+        if not self._replayed and not torch.cuda.is_current_stream_capturing():
+            self.max_comp_len = min(self.max_comp_len, bound)
+
+    def _readable(self) -> int:
+        """max_comp_len for a call that reads the prefix: a captured one reads what it finds at a
+        replay."""
+        return self.Tcap if torch.cuda.is_current_stream_capturing() else self.max_comp_len
+
+
+class RVQKVCache(_HostBound):
     """Compressed KV cache of one attention layer: RVQ codes for old tokens, an fp16 window for
     the newest ones.  prefill() encodes a prompt, append() inserts one token per sequence
     (evicting and encoding the oldest window token when the window is full), attend() runs one
@@ -1269,6 +1292,10 @@ class RVQKVCache:
     that each compressed token receives (in ``acc``, made by its first call) and evict() keeps the
     heaviest.  verify() and note_weights() share a workspace: calls and replayed graphs of them
     must not run at once.  All state lives on the GPU; lengths never leave the device.
+    Calls may be captured into graphs.  A replay works on the lengths that it finds: a captured
+    verify() or note_weights() reads up to the capacity, and once a call that changes the lengths has
+    been captured, so does every other call.  (A captured prefill() clears the totals if they are
+    there at the capture.)
     k_smooth: optional float32 [Hkv, d] key smoothing factors (the key codebooks must have been
     trained on smoothed keys)."""
 
@@ -1290,7 +1317,7 @@ class RVQKVCache:
         self.win_len = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.win_head = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.max_comp_len = 0      # host-side bound used to size decode launches
+        self.max_comp_len = 0      # host-side bound used to size launches
         self.acc = None            # float32 [batch, Hkv, Tcap] attention-weight totals
         self._ws = None
         self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
@@ -1314,7 +1341,7 @@ class RVQKVCache:
         self.comp_len.fill_(Tc)
         self.win_len.fill_(W)
         self.win_head.zero_()
-        self.max_comp_len = Tc
+        self._grown(Tc)
         if self.acc is not None:
             self.acc.zero_()
 
@@ -1323,7 +1350,7 @@ class RVQKVCache:
         rvq_append(k_new.contiguous(), v_new.contiguous(), self.win_k, self.win_v, self.win_len,
                    self.win_head, self.comp_len, self.k_codes, self.v_codes, self.Ck, self.Cv,
                    self.error_flag, self.k_smooth)
-        self.max_comp_len = min(self.max_comp_len + 1, self.Tcap)
+        self._grown(self.max_comp_len + 1)
 
     def attend(self, q: torch.Tensor, softmax_scale=None, out=None, lse=None):
         """q: fp16 [B, Hq, d] -> (out float32 [B, Hq, d], lse float32 [B, Hq])."""
@@ -1341,7 +1368,7 @@ class RVQKVCache:
         """append(k_new, v_new) then attend(q) as one library call (zkv_rvq_serve_step: the
         lookup tables are built beside the encode of the evicted token); the same results as
         the two calls.  k_new, v_new fp16 [B, Hkv, d]; q fp16 [B, Hq, d]."""
-        self.max_comp_len = min(self.max_comp_len + 1, self.Tcap)
+        self._grown(self.max_comp_len + 1)
         args = (q, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv, self.win_k,
                 self.win_v, self.win_len)
         need = decode_workspace_size(*args, max_comp_len=self.max_comp_len)
@@ -1371,7 +1398,7 @@ class RVQKVCache:
                 self.win_k, self.win_v, self.win_len)
         need = tree_workspace_size(*args)
         return rvq_tree_attn(*args, mask=mask, n_draft=n_draft, out=out, lse=lse,
-                             max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
+                             max_comp_len=self._readable(), softmax_scale=softmax_scale,
                              workspace=self._scratch(need), error_flag=self.error_flag,
                              k_smooth=self.k_smooth)
 
@@ -1382,7 +1409,7 @@ class RVQKVCache:
         rvq_tree_commit(draft_k, draft_v, path, n_accept, self.win_k, self.win_v, self.win_len,
                         self.win_head, self.comp_len, self.k_codes, self.v_codes, self.Ck, self.Cv,
                         self.error_flag, self.k_smooth)
-        self.max_comp_len = min(self.max_comp_len + path.shape[1], self.Tcap)
+        self._grown(self.max_comp_len + path.shape[1])
 
     def note_weights(self, q: torch.Tensor, lse: torch.Tensor, softmax_scale=None, n_draft=None):
         """Adds the attention weight of q over the compressed tokens to ``acc``
@@ -1397,7 +1424,7 @@ class RVQKVCache:
                                    device=self.k_codes.device)
         args = (q, lse, self.k_codes, self.comp_len, self.Ck, self.acc)
         need = weights_workspace_size(*args)
-        return rvq_accumulate_weights(*args, max_comp_len=self.max_comp_len,
+        return rvq_accumulate_weights(*args, max_comp_len=self._readable(),
                                       softmax_scale=softmax_scale, workspace=self._scratch(need),
                                       error_flag=self.error_flag, k_smooth=self.k_smooth,
                                       n_draft=n_draft)
@@ -1409,7 +1436,7 @@ class RVQKVCache:
             raise ValueError("evict() needs the totals that note_weights() makes")
         rvq_evict(self.k_codes, self.v_codes, self.comp_len, self.acc, keep, recent, kept=kept,
                   error_flag=self.error_flag)
-        self.max_comp_len = min(self.max_comp_len, int(keep))
+        self._shrunk(int(keep))
 
     def memory_bytes(self) -> int:
         """Bytes held by codes and window (codebooks are shared across layers' caches)."""
