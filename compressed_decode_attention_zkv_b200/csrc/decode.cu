@@ -137,7 +137,7 @@ static DecodePlan make_plan(const zkv_decode_params* p) {
   while (Rk > 1 && scan_smem_bytes(Rk, p->Sk, p->Sv, pl.GP, v) > kSmemMax) Rk >>= 1;
   pl.Rk = Rk;
   const int64_t pairs = (int64_t)p->B * p->Hkv;
-  const int64_t bound = pairs * p->max_comp_len;
+  const int64_t bound = pairs * (p->launch_len > 0 ? p->launch_len : p->max_comp_len);
   const int sms = sm_count();
   auto pow124 = [](int s) { return s == 1 || s == 2 || s == 4; };
   pl.scan2 = pow124(p->Sk) && pow124(p->Sv);
@@ -152,7 +152,7 @@ static DecodePlan make_plan(const zkv_decode_params* p) {
     pl.seg_cost = kSegCost;
     pl.cap = (int64_t)kColCap * v.J;
     // every CTA's virtual share (tokens + kSegCost per pair) stays below the column capacity
-    int64_t g1 = (bound + kSegCost * pairs + pl.cap - 1) / pl.cap;
+    int64_t g1 = (pairs * p->max_comp_len + kSegCost * pairs + pl.cap - 1) / pl.cap;
     int64_t g2 = std::min<int64_t>(sms, (bound + 1023) / 1024);
     int64_t grid = std::max<int64_t>(1, std::max(g1, g2));
     if (grid > sms) grid = (grid + sms - 1) / sms * sms;
@@ -1752,7 +1752,8 @@ static int validate_decode_shapes(const zkv_decode_params* p) {
   if (p->Sk < 1 || p->Sk > kMaxStages || p->Sv < 1 || p->Sv > kMaxStages) return ZKV_ERR_UNSUPPORTED;
   if (p->Hq / p->Hkv > 8) return ZKV_ERR_UNSUPPORTED;
   if (p->B > 65535 || p->Hkv > 65535 || (int64_t)p->B * p->Hkv > (1 << 24)) return ZKV_ERR_UNSUPPORTED;
-  if (p->Tcap < 0 || p->Wcap < 0 || p->max_comp_len < 0 || p->max_comp_len > p->Tcap)
+  if (p->Tcap < 0 || p->Wcap < 0 || p->max_comp_len < 0 || p->max_comp_len > p->Tcap ||
+      p->launch_len < 0 || p->launch_len > p->Tcap)
     return ZKV_ERR_INVALID_ARG;
   if (p->Tcap % 16) return ZKV_ERR_INVALID_ARG;
   if (p->Tcap > (int64_t(1) << 28)) return ZKV_ERR_UNSUPPORTED;   // 32-bit in-pair offsets

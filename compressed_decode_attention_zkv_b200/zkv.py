@@ -73,7 +73,7 @@ class DecodeParams(ctypes.Structure):
                 ("out", c_void_p), ("lse", c_void_p), ("error_flag", c_void_p),
                 ("trace_events", c_void_p), ("k_smooth", c_void_p),
                 ("block_table", c_void_p), ("page_tokens", c_int64), ("max_pages", c_int64),
-                ("n_pages", c_int64)]
+                ("n_pages", c_int64), ("launch_len", c_int64)]
 
 
 class AppendParams(ctypes.Structure):
@@ -395,7 +395,7 @@ def rvq_reconstruct(codes: torch.Tensor, codebooks: torch.Tensor, unrotate: bool
 
 def _decode_params(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win_k, win_v,
                    win_len, out, lse, max_comp_len, softmax_scale, error_flag,
-                   k_smooth=None, block_table=None) -> DecodeParams:
+                   k_smooth=None, block_table=None, launch_len=None) -> DecodeParams:
     _need(q, "q", torch.float16)
     _need(k_codes, "k_codes", torch.uint8)
     _need(v_codes, "v_codes", torch.uint8)
@@ -423,7 +423,8 @@ def _decode_params(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win_
                         v_codebooks=_ptr(v_codebooks), win_k=_ptr(win_k), win_v=_ptr(win_v),
                         win_len=_ptr(win_len), out=_ptr(out), lse=_ptr(lse),
                         error_flag=_ptr(error_flag),
-                        k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged)
+                        k_smooth=_smooth_ptr(k_smooth, Hkv, d, "k_smooth"), **paged,
+                        launch_len=0 if launch_len is None else int(launch_len))
 
 
 def decode_workspace_size(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win_k,
@@ -439,12 +440,13 @@ def decode_workspace_size(q, k_codes, v_codes, comp_len, k_codebooks, v_codebook
 def rvq_decode_attn(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win_k, win_v,
                     win_len, out=None, lse=None, max_comp_len=None, softmax_scale=None,
                     workspace: torch.Tensor | None = None, error_flag=None, trace_events=None,
-                    k_smooth=None, block_table=None):
+                    k_smooth=None, block_table=None, launch_len=None):
     """Decode attention over the compressed prefix plus the fp16 window (see include/zkv.h).
     ``trace_events``: optional 4 torch.cuda.Event(enable_timing=True) recorded before the
     table, scan and combine kernels and after the last one (graph nodes under capture).  ``k_smooth``: the [Hkv, d] key
     smoothing factors the prefix was encoded with.  ``block_table``: int32 [B, max_pages] for
     the paged layout (k_codes / v_codes are then page pools [n_pages, Hkv, P, S]).
+    ``launch_len``: the length that the launch is sized for, if not max_comp_len.
     Returns (out float32 [B, Hq, d], lse float32 [B, Hq])."""
     B, Hq, d = q.shape
     if out is None:
@@ -453,7 +455,7 @@ def rvq_decode_attn(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     p = _decode_params(q, k_codes, v_codes, comp_len, k_codebooks, v_codebooks, win_k, win_v,
                        win_len, out, lse, max_comp_len, softmax_scale, error_flag, k_smooth,
-                       block_table)
+                       block_table, launch_len)
     ev_arr = None
     if trace_events is not None:
         if len(trace_events) != 4:
@@ -1282,6 +1284,14 @@ class _HostBound:
         replay."""
         return self.Tcap if torch.cuda.is_current_stream_capturing() else self.max_comp_len
 
+    def _decode_scratch(self, need: int) -> torch.Tensor:
+        # outgrown ones are kept, as a captured graph may hold their addresses (the sizes go by the
+        # capacity, so only more heads than ever before outgrow one)
+        if self._ws is None or self._ws.numel() < need:
+            self._old_ws.append(self._ws)
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
+        return self._ws
+
 
 class RVQKVCache(_HostBound):
     """Compressed KV cache of one attention layer: RVQ codes for old tokens, an fp16 window for
@@ -1293,9 +1303,9 @@ class RVQKVCache(_HostBound):
     heaviest.  verify() and note_weights() share a workspace: calls and replayed graphs of them
     must not run at once.  All state lives on the GPU; lengths never leave the device.
     Calls may be captured into graphs.  A replay works on the lengths that it finds: a captured
-    verify() or note_weights() reads up to the capacity, and once a call that changes the lengths has
-    been captured, so does every other call.  (A captured prefill() clears the totals if they are
-    there at the capture.)
+    attend(), verify() or note_weights() reads up to the capacity, and once a call that changes the
+    lengths has been captured, so does every other call.  (A captured prefill() clears the totals
+    if they are there at the capture.)
     k_smooth: optional float32 [Hkv, d] key smoothing factors (the key codebooks must have been
     trained on smoothed keys)."""
 
@@ -1319,7 +1329,7 @@ class RVQKVCache(_HostBound):
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_comp_len = 0      # host-side bound used to size launches
         self.acc = None            # float32 [batch, Hkv, Tcap] attention-weight totals
-        self._ws = None
+        self._ws, self._old_ws = None, []     # workspace of attend() and step()
         self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
@@ -1356,12 +1366,13 @@ class RVQKVCache(_HostBound):
         """q: fp16 [B, Hq, d] -> (out float32 [B, Hq, d], lse float32 [B, Hq])."""
         args = (q, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv, self.win_k,
                 self.win_v, self.win_len)
-        need = decode_workspace_size(*args, max_comp_len=self.max_comp_len)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        return rvq_decode_attn(*args, out=out, lse=lse, max_comp_len=self.max_comp_len,
-                               softmax_scale=softmax_scale, workspace=self._ws,
-                               error_flag=self.error_flag, k_smooth=self.k_smooth)
+        # (a capture: sized for the present prefix, or a quarter of the capacity if that is longer)
+        return rvq_decode_attn(*args, out=out, lse=lse, max_comp_len=self._readable(),
+                               softmax_scale=softmax_scale,
+                               workspace=self._decode_scratch(decode_workspace_size(*args)),
+                               error_flag=self.error_flag, k_smooth=self.k_smooth,
+                               launch_len=max(self.max_comp_len, self.Tcap // 4)
+                               if torch.cuda.is_current_stream_capturing() else None)
 
     def step(self, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor,
              softmax_scale=None, out=None, lse=None):
@@ -1371,15 +1382,12 @@ class RVQKVCache(_HostBound):
         self._grown(self.max_comp_len + 1)
         args = (q, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv, self.win_k,
                 self.win_v, self.win_len)
-        need = decode_workspace_size(*args, max_comp_len=self.max_comp_len)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
         return rvq_serve_step(k_new.contiguous(), v_new.contiguous(), q, self.win_k, self.win_v,
                               self.win_len, self.win_head, self.comp_len, self.k_codes,
                               self.v_codes, self.Ck, self.Cv, out=out, lse=lse,
                               max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
-                              workspace=self._ws, error_flag=self.error_flag,
-                              k_smooth=self.k_smooth)
+                              workspace=self._decode_scratch(decode_workspace_size(*args)),
+                              error_flag=self.error_flag, k_smooth=self.k_smooth)
 
     def _scratch(self, need: int) -> torch.Tensor:
         # outgrown ones are kept: a captured graph may hold their addresses (the sizes go by the

@@ -75,7 +75,7 @@ const char* zkv_status_string(int status);
 /* Library ABI version (major * 100 + minor): 1.01 adds the serving step, the paged layout,
  * key smoothing, product VQ and the context-parallel combines to 1.00's encode / decode; 1.02
  * the tree attention, the path commit, the attention-weight totals and the eviction; 1.03
- * n_draft of the attention-weight totals. */
+ * n_draft of the attention-weight totals and launch_len of the decode. */
 #define ZKV_VERSION 103
 int zkv_version(void);
 
@@ -224,6 +224,11 @@ typedef struct {
    * across sequences that never write them.  NULL: the contiguous layout above. */
   const int32_t* block_table;
   int64_t page_tokens, max_pages, n_pages;
+  /* 0, or the length (<= Tcap) that the launch is sized for instead of max_comp_len, which then only
+   * bounds what is read: for a captured call, whose replays meet lengths that are not known yet.
+   * Any value gives correct results; blocks are too few for much longer prefixes, too many for
+   * much shorter ones. */
+  int64_t launch_len;
 } zkv_decode_params;
 
 /* Workspace bytes for a call with these shapes (data pointers are not read); 0 if the shapes

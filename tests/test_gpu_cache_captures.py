@@ -1,5 +1,7 @@
 """Captured calls of the cache class: what a graph records runs again at every replay, when the
 prefix has another length than at the capture."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -142,6 +144,22 @@ def test_replayed_decoding_sees_the_tokens_that_it_appends(how):
     close(a.attend(q)[0], b.attend(q)[0])
 
 
+def test_a_replayed_attend_sees_what_eager_calls_append():
+    (a, b), new = twins(84, T=700, capacity=4096)
+    k, v, q = new(2, HKV, DIM), new(2, HKV, DIM), new(2, HQ, DIM)
+    first, _ = a.attend(q)
+    got = torch.zeros(2, HQ, DIM, device="cuda")
+    g = captured(lambda: a.attend(q, out=got))
+    g.replay()
+    assert torch.equal(got, first)
+    long = new(2, HKV, 3500, DIM)
+    for c in (a, b):
+        c.prefill(long, long)
+    g.replay()
+    close(got, b.attend(q)[0])
+    assert math.isfinite(got.sum().item())
+
+
 def test_a_captured_prefill_is_counted_at_every_replay():
     (a, b), new = twins(85, T=300)
     k, v, q = new(2, HKV, 300, DIM), new(2, HKV, 300, DIM), new(2, HQ, DIM)
@@ -152,3 +170,44 @@ def test_a_captured_prefill_is_counted_at_every_replay():
     b.prefill(k, v)
     same_state(a, b)
     close(a.attend(q)[0], b.attend(q)[0])
+
+
+def test_a_captured_attend_outlives_more_heads():
+    """A graph of attend() keeps its workspace when later calls need a larger one."""
+    (a, b), new = twins(86, T=500)
+    q, wide = new(2, HKV, DIM), new(2, HKV * 4, DIM)       # one head per kv head, then four
+    first, _ = a.attend(q)
+    got = torch.zeros_like(first)
+    g = captured(lambda: a.attend(q, out=got))
+    size = a._ws.numel()
+    a.attend(wide)
+    assert a._ws.numel() > size
+    # memory of that size that the call above may have given back, filled
+    fill = [torch.full((size,), 165, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, first)
+    for f in fill:
+        assert (f == 165).all()
+
+
+@pytest.mark.parametrize("Sk,Sv,Hq", [(4, 4, 8), (3, 2, 2), (1, 5, 4)])
+def test_any_launch_length_gives_the_same_attention(Sk, Sv, Hq):
+    """Launches sized for far less and far more than the lengths that they meet."""
+    rng = np.random.default_rng(87)
+    Bn, T, d = 3, 9008, 64
+    c = lambda a: torch.from_numpy(a).cuda()   # noqa: E731
+    books = [c((rng.standard_normal((1, s, 256, d)) * 0.4).astype(np.float32)) for s in (Sk, Sv)]
+    kc, vc = (c(rng.integers(0, 256, (Bn, 1, T, s)).astype(np.uint8)) for s in (Sk, Sv))
+    q, wk, wv = (c(rng.standard_normal(s).astype(np.float16)) for s in ((Bn, Hq, d), (Bn, 1, 16, d), (Bn, 1, 16, d)))
+    comp, win = c(np.array([9001, 0, 1025], np.int32)), c(np.array([16, 3, 0], np.int32))
+    args = (q, kc, vc, comp, *books, wk, wv, win)
+    want, want_lse = zkv.rvq_decode_attn(*args)
+    for n in (1, 1000, 5000, 9008):
+        out, lse = zkv.rvq_decode_attn(*args, launch_len=n)
+        close(out, want)
+        close(lse, want_lse)
+        assert n < 9008 or torch.equal(out, want)
+    for n in (-1, 9009):
+        with pytest.raises(zkv.ZkvError):
+            zkv.rvq_decode_attn(*args, launch_len=n)
