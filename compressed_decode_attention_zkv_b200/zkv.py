@@ -1452,11 +1452,11 @@ class RVQKVCache(_HostBound):
                    (self.k_codes, self.v_codes, self.win_k, self.win_v))
 
 
-class PQKVCache:
+class PQKVCache(_HostBound):
     """Product-VQ (VecInfer-style) compressed KV cache of one attention layer: d/m code bytes
     per token for K and for V (one 256-entry codebook of m-dim sub-vectors per kv head and K or
     V), an fp16 window for the newest tokens.  The same interface as RVQKVCache: prefill(),
-    append(), attend(), step(), memory_bytes().  k_smooth: optional float32 [Hkv, d] key
+    append(), attend(), step(), memory_bytes(), captured calls included.  k_smooth: optional float32 [Hkv, d] key
     smoothing factors (the key codebooks must have been trained on smoothed keys)."""
 
     def __init__(self, k_codebook: torch.Tensor, v_codebook: torch.Tensor, batch: int,
@@ -1481,7 +1481,7 @@ class PQKVCache:
         self.win_head = torch.zeros(batch, dtype=torch.int32, device=dev)
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_comp_len = 0
-        self._ws = None
+        self._ws, self._old_ws = None, []
         self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
@@ -1502,25 +1502,22 @@ class PQKVCache:
         self.comp_len.fill_(Tc)
         self.win_len.fill_(W)
         self.win_head.zero_()
-        self.max_comp_len = Tc
+        self._grown(Tc)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor):
         """k_new, v_new: fp16 [B, Hkv, d]."""
         pq_append(k_new.contiguous(), v_new.contiguous(), self.win_k, self.win_v, self.win_len,
                   self.win_head, self.comp_len, self.k_codes, self.v_codes, self.Ck, self.Cv,
                   self.error_flag, self.k_smooth)
-        self.max_comp_len = min(self.max_comp_len + 1, self.Tcap)
+        self._grown(self.max_comp_len + 1)
 
     def attend(self, q: torch.Tensor, softmax_scale=None, out=None, lse=None):
         """q: fp16 [B, Hq, d] -> (out float32 [B, Hq, d], lse float32 [B, Hq])."""
-        need = pq_decode_workspace_size(q, self.k_codes, self.Ck, self.win_k,
-                                        max_comp_len=self.max_comp_len)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        need = pq_decode_workspace_size(q, self.k_codes, self.Ck, self.win_k)
         return pq_decode_attn(q, self.k_codes, self.v_codes, self.comp_len, self.Ck, self.Cv,
                               self.win_k, self.win_v, self.win_len, out=out, lse=lse,
-                              max_comp_len=self.max_comp_len, softmax_scale=softmax_scale,
-                              workspace=self._ws, error_flag=self.error_flag,
+                              max_comp_len=self._readable(), softmax_scale=softmax_scale,
+                              workspace=self._decode_scratch(need), error_flag=self.error_flag,
                               k_smooth=self.k_smooth)
 
     def step(self, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor,

@@ -211,3 +211,67 @@ def test_any_launch_length_gives_the_same_attention(Sk, Sv, Hq):
     for n in (-1, 9009):
         with pytest.raises(zkv.ZkvError):
             zkv.rvq_decode_attn(*args, launch_len=n)
+
+
+def pq_twins(seed, T, capacity):
+    rng = np.random.default_rng(seed)
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float16)).cuda()   # noqa: E731
+    books = [torch.from_numpy(rng.standard_normal((HKV, 256, 4)).astype(np.float32)).cuda() for _ in range(2)]
+    caches = [zkv.PQKVCache(*books, batch=2, capacity=capacity, window=16, head_dim=DIM) for _ in range(2)]
+    k, v = new(2, HKV, T, DIM), new(2, HKV, T, DIM)
+    for c in caches:
+        c.prefill(k, v)
+    return caches, new
+
+
+@pytest.mark.parametrize("what", ["attend", "append and attend"])
+def test_product_vq_replays_see_the_tokens_that_are_there(what):
+    (a, b), new = pq_twins(88, T=60, capacity=4096)
+    k, v, q = new(2, HKV, DIM), new(2, HKV, DIM), new(2, HQ, DIM)
+    for c in (a, b):
+        c.step(k, v, q)
+    got = torch.zeros(2, HQ, DIM, device="cuda")
+
+    def step():
+        if what != "attend":
+            a.append(k, v)
+        a.attend(q, out=got)
+    g = captured(step)
+    for i in range(40):
+        for x in (k, v, q):
+            x.copy_(new(*x.shape))
+        if what == "attend":
+            a.append(k, v)
+        g.replay()
+        want, _ = b.step(k, v, q)
+        close(got, want)
+    same_state(a, b)
+    long = new(2, HKV, 4000, DIM)
+    for c in (a, b):
+        c.prefill(long, long)
+    g.replay()
+    if what != "attend":
+        b.append(k, v)
+    close(got, b.attend(q)[0])
+    g.replay()                               # and once more than eager calls know of
+    if what != "attend":
+        b.append(k, v)
+    same_state(a, b)
+    close(a.attend(q)[0], b.attend(q)[0])
+
+
+def test_a_captured_product_vq_attend_outlives_more_heads():
+    (a, b), new = pq_twins(89, T=500, capacity=1024)
+    q, wide = new(2, HKV, DIM), new(2, HKV * 4, DIM)
+    first, _ = a.attend(q)
+    got = torch.zeros_like(first)
+    g = captured(lambda: a.attend(q, out=got))
+    size = a._ws.numel()
+    a.attend(wide)
+    assert a._ws.numel() > size
+    fill = [torch.full((size,), 165, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, first)
+    for f in fill:
+        assert (f == 165).all()
