@@ -1482,7 +1482,6 @@ class PQKVCache(_HostBound):
         self.error_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_comp_len = 0
         self._ws, self._old_ws = None, []
-        self._tree_ws = []         # workspaces of verify() and note_weights(), the last one in use
 
     def prefill(self, k: torch.Tensor, v: torch.Tensor):
         """k, v: fp16 [B, Hkv, T, d].  The last min(T, window) tokens go to the window, the
