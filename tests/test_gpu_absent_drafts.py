@@ -24,8 +24,9 @@ def _cuda(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
-def _totals(cache, q, dk, nd, before):
-    """float64 totals after the attention of the present drafts (a chain) over the cache."""
+def _totals(cache, q, dk, nd, before, counts=None):
+    """float64 totals after the attention of the present drafts (a chain) over the cache; of those
+    that ``counts`` [B, N] names, if it is given."""
     q, dk = q.double().cpu().numpy(), dk.double().cpu().numpy()
     kc, wk = cache.k_codes.cpu().numpy(), cache.win_k.double().cpu().numpy()
     comp, win = cache.comp_len.cpu().numpy(), cache.win_len.cpu().numpy()
@@ -42,7 +43,8 @@ def _totals(cache, q, dk, nd, before):
                 x = q[b, :m, g] @ k.T / math.sqrt(d)
                 x[:, n + w:][np.arange(m)[None] > np.arange(m)[:, None]] = -np.inf
                 p = np.exp(x - x.max(1, keepdims=True))
-                acc[b, h, :n] += (p / p.sum(1, keepdims=True))[:, :n].sum(0)
+                p /= p.sum(1, keepdims=True)
+                acc[b, h, :n] += p[slice(None) if counts is None else counts[b, :m], :n].sum(0)
     return acc
 
 
@@ -103,3 +105,29 @@ def test_n_draft_is_checked():
         zkv.rvq_accumulate_weights(*args, n_draft=torch.ones(3, dtype=torch.int32, device="cuda"))
     with pytest.raises(TypeError):
         zkv.rvq_accumulate_weights(*args, n_draft=torch.ones(2, device="cuda"))
+
+
+def test_accepted_drafts_alone_count():
+    """verify, note_weights of the accepted rows, commit, evict, as a serving loop runs them."""
+    cache, drafts = _filled_cache(np.random.default_rng(75))
+    acc = np.zeros((cache.B, cache.Hkv, cache.Tcap))
+    path = torch.tensor([[0, 2, 3], [0, 1, 0]], dtype=torch.int32, device="cuda")
+    n_accept = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    accepted = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    accepted[0, [0, 2, 3]] = accepted[1, [0, 1]] = True
+    for _ in range(3):
+        q, dk, dv = drafts(4)
+        out, lse = cache.verify(q, dk, dv)
+        acc = _totals(cache, q, dk, [4, 4], acc, accepted.cpu().numpy())
+        cache.note_weights(q, lse.masked_fill(~accepted[:, :, None], float("inf")))
+        assert np.abs(cache.acc.double().cpu().numpy() - acc).max() < 3e-4 * (1 + acc.max())
+        cache.commit(dk, dv, path, n_accept)
+    old = cache.comp_len.cpu().numpy()
+    kept = torch.zeros(2, cache.Hkv, 300, dtype=torch.int32, device="cuda")
+    cache.evict(300, recent=50, kept=kept)
+    kept = kept.cpu().numpy()
+    for b in range(2):
+        for h in range(cache.Hkv):
+            t = np.setdiff1d(np.arange(old[b] - 50), kept[b, h])      # an old token that went is no heavier
+            k = kept[b, h][kept[b, h] < old[b] - 50]
+            assert len(k) == 250 and acc[b, h, t].max() <= acc[b, h, k].min() + 6e-4 * (1 + acc.max())
