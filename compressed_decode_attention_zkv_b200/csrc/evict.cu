@@ -16,10 +16,13 @@
 //   3. Copy.  Kept neighbours go to neighbouring places.  In place, a CTA first collects its kept
 //      rows in shared memory, four bytes of each at a time, and writes after a cluster barrier: by
 //      then every source of the (sequence, kv head) has been read.
-// 64 (sequence, kv head)s of 32640 tokens, an eighth kept: 18.5 us; 4 of 130816, a quarter kept: 23 us; one
-// of 960: 10 us.  Chains of latency bound it (cycles of one CTA of 16320 tokens: totals in 3600, three
-// passes 3500 to 4500 each, a cluster barrier and remote counts in each; flags and offsets 1700, sources
-// 3000, copies 3800), not bytes (14.6 MB: 12 % of the copy bandwidth).
+// A call in a graph, inputs larger than the L2 except the last: 64 (sequence, kv head)s of 32640 tokens, an
+// eighth kept, 4 + 4 stages: 19.7 us to other buffers (pages: 22.0), 26.2 us in place (pages: 29.6); 4 of
+// 130816, a quarter kept, 2 + 4 stages: 22.4 (28.8) and 32.3 (37.0); one of 960: 8.2 (9.9) and 11.1 (11.6).
+// In place a turn per four bytes of a row, each with a cluster barrier, and the kernel that writes the
+// lengths come on top.  Chains of latency bound it (cycles of one CTA of 16320 tokens, to other buffers:
+// totals in 3600, three passes 3500 to 4500 each, a cluster barrier and remote counts in each; flags and
+// offsets 1700, sources 3000, copies 3800), not bytes (14.6 MB: 11 % of the copy bandwidth).
 // The cluster has as many CTAs as the range needs and, up to 8, as leave no SM without work.
 #include <cooperative_groups.h>
 

@@ -22,12 +22,14 @@
 // passes of 128 bytes, gathers and counter additions together.  Reconstructing its key and value for
 // float32-accurate matrix products costs (Sk + Sv) d / 32 passes to gather float32 codewords and d / 16
 // to write the split vectors, whatever R is, and the codebooks of more than one stage do not fit in
-// shared memory.  So the histogram form is the cheaper one up to about R = d.
+// shared memory.  So the histogram form is the cheaper one up to about R = d.  Wider trees take it too: the
+// other form would be the cheaper one there by this count, and has not been built.
 //
-// Measured (B200): 8 sequences x 32640 tokens, 32 / 8 heads, d = 128, 4 + 4 stages, 16 drafts: 262 us a
-// call (split 6, tables 18, dense 15, scan 209, contraction 24, finish 8, partly side by side); one
-// sequence x 130816 tokens, 28 / 4 heads, 2 + 4 stages, 25 drafts: 149 us; 64 ragged sequences of 1024
-// .. 16384 tokens, 5 drafts: 361 us; one head, 960 tokens, 8 drafts: 25 us, five launches' latency.
+// Measured (B200), a call among others: 8 sequences x 32640 tokens, 32 / 8 heads, d = 128, 4 + 4 stages,
+// 16 drafts 264 us (split 7, tables 20, dense 17, scan 209, contraction 27, finish 9, each alone and cold;
+// partly side by side); one sequence x 130816 tokens, 28 / 4 heads, 2 + 4 stages, 25 drafts 148 us;
+// 64 ragged sequences of 1024 .. 16384 tokens, 5 drafts 369 .. 382 us; one head, 960 tokens, 8 drafts 26 us,
+// the latency of five dependent launches.  Rows of absent drafts are scanned and contracted like others.
 #include "query_tables.cuh"
 #include "tree_tables_tc.cuh"
 
@@ -446,7 +448,8 @@ __global__ void __launch_bounds__(kTtThreads, 1) tree_tables_tc_kernel(TreeArgs 
 // folded against its own maximum as the new ref.
 //
 // Bound: the shared-memory pipe.  At 8 x 32640 tokens, 64 rows: 209 us, 76 % of its passes used (40.5 M
-// of gathers, code reads and additions), 57 % of the issue slots, 2 CTAs of 12 warps per SM.  Steps
+// of gathers, code reads and additions, 42.7 M with the copies), 57 % of the issue slots, 2 CTAs of 12 warps
+// per SM.  Steps
 // measured on that case: one row per lane 275 us; two rows per lane (half the address permutations and
 // code reads) with the codes copied ahead into shared memory instead of registers 185 us beside the
 // tables; 8 instead of 12 warps 6 % slower; 8 instead of 16 tokens per thread 30 % slower (the exchange

@@ -27,10 +27,12 @@
 // One such codeword is the choice (for Gaussian codewords 15 times of 16); several are told apart by
 // float64 distances, ties to the lowest index, as zkv_rvq_encode decides.
 // Chunks take turns in two buffers, so one is rounded while another's products run: one barrier a chunk.
-// 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages: 24.7 us; 64 sequences, up to 5: 39 us
-// (one buffer: 28 and 43; a cluster of 8 CTAs per 8 evictions, float32 distances: 50 and 176 us); one
-// head, 2 + 2 stages: 14 us.  The length update after it adds 1 us to each.
-// Bound by a block's chain: per chunk its rounding and products, per stage the decision.
+// A call (both kernels) in a graph: 8 sequences, up to 6 tokens each, 8 kv heads, d = 128, 4 + 4 stages
+// 26.9 us; 64 sequences, up to 5 each 40.6 us; one head, 2 + 2 stages 12.3 us; pages or smoothing up to
+// 1.2 us more.  (The second buffer gained 3 us in the batches; a cluster of 8 CTAs per 8 evictions with
+// float32 distances took 50 and 176 us.)
+// Bound by a block's chain: per chunk its rounding and products, per stage the decision.  In the batch of
+// 64 six to ten blocks of a head convert the same codewords.
 #include <cfloat>
 #include <cmath>
 

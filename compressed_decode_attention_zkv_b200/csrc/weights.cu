@@ -18,8 +18,8 @@
 // modulo 128 bytes, of their codewords' rows (they start at different stages, row halves or copies),
 // so a gather has no bank conflict whatever the codes are.
 //
-// 8 sequences x 32640 tokens, 32 / 8 heads, 4 stages: 18.5 us a call (29.3 MB: 25 % of the copy
-// bandwidth), tables 8 us and scan 11 us; 130816 tokens, 28 / 4 heads, 2 stages: 10.4 us.  The tables'
+// A call among others: 8 sequences x 32640 tokens, 32 / 8 heads, 4 stages 18.4 us (29.3 MB: 25 % of the
+// copy bandwidth), tables 8 us and scan 11 us; 130816 tokens, 28 / 4 heads, 2 stages 10.3 us.  The tables'
 // latency and one block's chain (tables in, 8 tokens a thread, totals in and out) bound it.
 #include "query_tables.cuh"
 
